@@ -314,6 +314,149 @@ mk_status mk_plan_schedule(const mk_config* cfg, int n_ctas, int batch,
                            const int32_t* seq_lens, const int32_t* plan_len,
                            int32_t* meta, int32_t* desc, int32_t* targets);
 
+/* ------------------------------------------------------------------------
+ * Serving operators beside the decode step.  They need no context: every
+ * tensor and size is an argument, each call launches on `stream` and returns.
+ * Conventions, next to those at the top of this file:
+ *  - `device` is the ordinal of the device that owns every pointer and the
+ *    stream; the caller's current device is put back before the call returns.
+ *  - `status` is NULL or a device int32[8] that the caller zeroed: the first
+ *    device-side fault of any call that names it is latched there as {code,
+ *    operator, entry, value, limit} with code MK_ERR_DEVICE (MK_ERR_TIMEOUT if a
+ *    device-side wait ran out: the call's output is then unusable); the
+ *    operator numbers are those of mk_op_id.  Faulty entries are left out,
+ *    the others are computed.
+ *  - Nothing is allocated and nothing is kept between calls, so calls may
+ *    overlap on different streams and be captured into graphs, as long as
+ *    their output and workspace memory does not overlap.                    */
+typedef enum mk_dtype { MK_FP32 = 0, MK_BF16 = 1, MK_FP16 = 2 } mk_dtype;
+
+enum mk_op_id { MK_OP_ROPE_APPEND = 1, MK_OP_PREFIX_ATTENTION = 2, MK_OP_SAMPLE = 3 };
+
+/* Rotate keys and append them with their values to a layer's paged cache;
+ * rotate queries on the way.
+ *   q, k, v     [n_tokens] rows of n_q_heads / n_kv_heads heads of head_dim
+ *               (64 or 128) consecutive elements of src_type (any mk_dtype);
+ *               strides between tokens and heads in elements, so the three
+ *               may be parts of one projection row.  n_q_heads 0: no queries.
+ *   q_out       [n_tokens][n_q_heads][head_dim] of dst_type (bf16 or fp16);
+ *               may be q itself when the types and strides agree
+ *   k_pool, v_pool  [n_pages][n_kv_heads][64][head_dim] of dst_type
+ *   positions   int32[n_tokens]: rotation angle and place in the cache
+ *   seq         int32[n_tokens]: the page-table row of each token, -1 for
+ *               padding (nothing of it is written); NULL: token t is row t
+ *   page_table  int32[n_rows][max_pages]: logical page -> physical page
+ *   inv_freq    float64[rotary_dim / 2]: angle per position of each pair
+ * Pair i of a head is columns (i, rotary_dim / 2 + i), or (2 i, 2 i + 1) with
+ * interleaved != 0; it turns by positions[t] * inv_freq[i] and is scaled by
+ * `magnitude`; columns from rotary_dim (even, 0 .. head_dim) on are copied.
+ * Scaled frequencies for stretched contexts are the caller's inv_freq.
+ * A sequence's row, position or page out of range is a device-side fault.
+ * Two tokens with the same sequence and position leave either one's rows.
+ * q_out and the pools are 16-byte aligned.                                  */
+typedef struct mk_rope_append_args {
+  int32_t device;
+  int32_t n_tokens, n_rows, max_pages, n_pages;
+  int32_t n_q_heads, n_kv_heads, head_dim, rotary_dim;
+  int32_t interleaved;
+  int32_t src_type, dst_type;
+  float magnitude;
+  const void *q, *k, *v;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
+      v_head_stride;
+  void *q_out, *k_pool, *v_pool;
+  const double* inv_freq;
+  const int32_t *positions, *seq, *page_table;
+  int32_t* status;
+} mk_rope_append_args;
+mk_status mk_rope_append(const mk_rope_append_args* args, void* stream);
+
+/* Attention of one query token per batch entry over the paged cache, for
+ * batches whose entries share prefixes: the shared tokens are read once for
+ * all of a group's entries.
+ *   q           [batch] rows of n_q_heads heads of head_dim (64 or 128)
+ *               elements of `type` (bf16 or fp16); token stride in elements (a
+ *               multiple of 8), heads adjacent; 16-byte aligned
+ *   k_pool, v_pool  [n_pages][n_kv_heads][64][head_dim], rotated keys
+ *   page_table  int32[batch][max_pages]
+ *   positions   int32[batch]: entry b attends to tokens 0 .. positions[b] of
+ *               its sequence, its own included (it must be in the cache); -1:
+ *               to none, its output is zero and its lse -infinity
+ *   group_start int32[n_groups + 1]: group g is entries group_start[g] ..
+ *               group_start[g + 1] - 1 (non-decreasing); entries of no group
+ *               (before the first or behind the last) are left as they were
+ *   prefix_lens int32[n_groups]: tokens 0 .. prefix_lens[g] - 1 of every entry
+ *               of the group are read through the page-table row of the
+ *               group's first entry; tokens from there on through the entry's
+ *               own row.  Any length, inside a page too; 0 shares nothing
+ *   out         [batch][n_q_heads][head_dim] of `type`
+ *   lse         NULL or float32[batch][n_q_heads]: log of the sum of exp of
+ *               the scaled scores
+ *   scale       factor of the scores (1 / sqrt(head_dim) is usual)
+ *   workspace   device memory of workspace_bytes, 256-byte aligned, at least
+ *               mk_prefix_attention_workspace(args); contents do not matter
+ * Entries of one sequence with increasing positions are a causal piece of a
+ * prompt: give the group a prefix that covers them all.  Group bounds out of
+ * order, a position outside the page table or a page id out of range is a
+ * device-side fault (the entry or page contributes nothing).  n_q_heads is a
+ * multiple of n_kv_heads, at most 64 times it; batch is at most 4096.       */
+typedef struct mk_prefix_attention_args {
+  int32_t device;
+  int32_t batch, n_groups, max_pages, n_pages;
+  int32_t n_q_heads, n_kv_heads, head_dim;
+  int32_t type;
+  float scale;
+  const void* q;
+  int64_t q_token_stride;
+  const void *k_pool, *v_pool;
+  const int32_t *page_table, *positions, *group_start, *prefix_lens;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* status;
+} mk_prefix_attention_args;
+size_t mk_prefix_attention_workspace(const mk_prefix_attention_args* args);
+mk_status mk_prefix_attention(const mk_prefix_attention_args* args, void* stream);
+
+/* Draw one token per row of logits from given uniform numbers.
+ *   logits      [batch] rows of `vocab` elements of `type`, row_stride apart
+ *   u           float32[batch], each in [0, 1)
+ *   temperature float32[batch] >= 0, or NULL for 1; 0 picks the largest logit
+ *   top_k       int32[batch] or NULL; <= 0: no limit
+ *   top_p       float32[batch] or NULL; >= 1: no limit
+ *   min_p       float32[batch] or NULL; <= 0: no limit
+ *   tokens      int32[batch]
+ *   logprobs    NULL or float32[batch]: log-probability of the drawn token
+ *               among the kept ones
+ * With w = exp((logit - largest) / temperature) in 64 bits and the tokens in
+ * descending order of their logits (equal ones by ascending id), the kept
+ * tokens are those of the first top_k whose preceding sum of w stays below
+ * top_p of the first top_k's sum, and whose own w is at least min_p; the
+ * first is always kept.  The drawn token is the first, by ascending id, at
+ * which the kept tokens' running sum of w passes u times their whole sum.
+ * NaN logits count as -infinity, which is never drawn; where a logit is
+ * +infinity only such are drawn, each with w = 1.  A row without a finite or
+ * positive infinite logit gives token -1 and logprob -infinity.  So does a row whose
+ * temperature is negative or not finite, whose u is outside [0, 1), or whose
+ * top_p or min_p is NaN: a device-side fault.
+ * vocab is at most MK_SAMPLE_MAX_VOCAB.                                     */
+#define MK_SAMPLE_MAX_VOCAB 409600
+typedef struct mk_sample_args {
+  int32_t device;
+  int32_t batch, vocab;
+  int32_t type;
+  const void* logits;
+  int64_t row_stride;
+  const float *u, *temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p;
+  int32_t* tokens;
+  float* logprobs;
+  int32_t* status;
+} mk_sample_args;
+mk_status mk_sample(const mk_sample_args* args, void* stream);
+
 const char* mk_strerror(mk_status s);
 
 /* Release everything the context owns (not the caller's tensors). */

@@ -9,7 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_size_t, c_void_p
+from ctypes import (POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t,
+                    c_void_p)
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmk.so")
 
@@ -21,6 +22,9 @@ MK_BUF_NSLOTS, MK_BUF_EXPERT_A, MK_BUF_MOE, MK_BUF_OPART = 5, 6, 7, 8
 MK_BUF_TRACE, MK_BUF_PLAN = 9, 10
 MK_STATIC_SCRATCH_MAX_BYTES = 32 * 1024 * 1024
 TRACE_WORDS = 18
+MK_FP32, MK_BF16, MK_FP16 = 0, 1, 2
+MK_OP_ROPE_APPEND, MK_OP_PREFIX_ATTENTION, MK_OP_SAMPLE = 1, 2, 3
+MK_SAMPLE_MAX_VOCAB = 409600
 
 # every entry point the header declares (checked by the ABI test)
 EXPORTS = (
@@ -28,7 +32,8 @@ EXPORTS = (
     "mk_decode_step_unfused", "mk_decode_step_static",
     "mk_check", "mk_selftest_timeout", "mk_set_timeout_ms", "mk_set_trace", "mk_debug_read",
     "mk_debug_size",
-    "mk_plan_schedule", "mk_strerror", "mk_destroy",
+    "mk_plan_schedule", "mk_rope_append", "mk_prefix_attention_workspace",
+    "mk_prefix_attention", "mk_sample", "mk_strerror", "mk_destroy",
 )
 
 
@@ -63,6 +68,33 @@ class mk_tensors(ctypes.Structure):
     ]
 
 
+class mk_rope_append_args(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in (
+        "device", "n_tokens", "n_rows", "max_pages", "n_pages", "n_q_heads", "n_kv_heads",
+        "head_dim", "rotary_dim", "interleaved", "src_type", "dst_type")] + [
+        ("magnitude", c_float)] + [(n, c_void_p) for n in ("q", "k", "v")] + [
+        (n, c_int64) for n in ("q_token_stride", "q_head_stride", "k_token_stride",
+                               "k_head_stride", "v_token_stride", "v_head_stride")] + [
+        (n, c_void_p) for n in ("q_out", "k_pool", "v_pool", "inv_freq", "positions", "seq",
+                                "page_table", "status")]
+
+
+class mk_prefix_attention_args(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in (
+        "device", "batch", "n_groups", "max_pages", "n_pages", "n_q_heads", "n_kv_heads",
+        "head_dim", "type")] + [("scale", c_float), ("q", c_void_p), ("q_token_stride", c_int64)] + [
+        (n, c_void_p) for n in ("k_pool", "v_pool", "page_table", "positions", "group_start",
+                                "prefix_lens", "out", "lse", "workspace")] + [
+        ("workspace_bytes", c_size_t), ("status", c_void_p)]
+
+
+class mk_sample_args(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("device", "batch", "vocab", "type")] + [
+        ("logits", c_void_p), ("row_stride", c_int64)] + [
+        (n, c_void_p) for n in ("u", "temperature", "top_k", "top_p", "min_p", "tokens",
+                                "logprobs", "status")]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(
@@ -85,6 +117,10 @@ def _load():
         "mk_debug_size": (c_size_t, [c_void_p, c_int]),
         "mk_plan_schedule": (c_int, [P(mk_config), c_int, c_int, P(c_int32), P(c_int32),
                                      P(c_int32), P(c_int32), P(c_int32)]),
+        "mk_rope_append": (c_int, [P(mk_rope_append_args), c_void_p]),
+        "mk_prefix_attention_workspace": (c_size_t, [P(mk_prefix_attention_args)]),
+        "mk_prefix_attention": (c_int, [P(mk_prefix_attention_args), c_void_p]),
+        "mk_sample": (c_int, [P(mk_sample_args), c_void_p]),
         "mk_strerror": (c_char_p, [c_int]),
         "mk_destroy": (None, [c_void_p]),
     }

@@ -1,0 +1,311 @@
+"""Serving operators beside the decode step: appending rotated keys and values
+to the paged cache, attention over prefixes that batch entries share, and
+sampling.
+
+Each function checks its arguments, hands raw device pointers to ``libmk.so``
+and returns after the launch; all computation happens in the library's
+kernels.  Tensors live on one CUDA device, which need not be the current one;
+``stream`` is a torch stream of that device (its current stream by default).
+A call keeps nothing: it may be captured into a graph, and calls on other
+streams may overlap it as long as they write other tensors.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from ctypes import byref, c_void_p
+from typing import Optional
+
+import torch
+
+from . import mk
+
+PAGE = 64
+
+_TYPE = {torch.float32: mk.MK_FP32, torch.bfloat16: mk.MK_BF16, torch.float16: mk.MK_FP16}
+_I32 = torch.int32
+_OPS = {mk.MK_OP_ROPE_APPEND: "rope_append", mk.MK_OP_PREFIX_ATTENTION: "prefix_attention",
+        mk.MK_OP_SAMPLE: "sample"}
+
+
+class Status:
+    """Device word that latches the first device-side fault of the calls that
+    name it (``status=``): a page id, position or parameter out of range."""
+
+    def __init__(self, device):
+        self.word = torch.zeros(8, dtype=_I32, device=device)
+
+    def check(self):
+        """Synchronize, read and clear: (status, [operator, entry, value, limit])."""
+        w = self.word.tolist()
+        if w[0] != mk.MK_OK:
+            self.word.zero_()
+        return w[0], w[1:5]
+
+    def check_ok(self) -> None:
+        rc, detail = self.check()
+        if rc != mk.MK_OK:
+            raise mk.MKError(rc, _OPS.get(detail[0], "device status"), detail)
+
+
+def _index(t: torch.Tensor, name: str, dev, shape) -> int:
+    if t.dtype != _I32 or t.device != dev:
+        raise TypeError(f"{name} must be an int32 tensor on {dev}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _float(t: torch.Tensor, name: str, dev, shape) -> int:
+    if t.dtype != torch.float32 or t.device != dev:
+        raise TypeError(f"{name} must be a float32 tensor on {dev}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _cuda(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _stream(stream, dev) -> c_void_p:
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    return c_void_p(s.cuda_stream)
+
+
+def _status(status: Optional[Status], dev):
+    if status is None:
+        return None
+    if status.word.device != dev:
+        raise ValueError(f"status must be on {dev}")
+    return status.word.data_ptr()
+
+
+def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor, dev):
+    """Checks one layer's pools; returns their shape (pages, heads, head size)."""
+    if k_pool.dtype not in (torch.bfloat16, torch.float16) or v_pool.dtype != k_pool.dtype:
+        raise TypeError("k_pool and v_pool must both be bfloat16 or both float16")
+    if k_pool.device != dev or v_pool.device != dev:
+        raise TypeError(f"k_pool and v_pool must be on {dev}")
+    shape = k_pool.shape
+    if len(shape) != 4 or v_pool.shape != shape or shape[2] != PAGE or shape[3] not in (64, 128):
+        raise ValueError("k_pool and v_pool must be [pages][kv heads][64][64 or 128]")
+    if not k_pool.is_contiguous() or not v_pool.is_contiguous():
+        raise ValueError("k_pool and v_pool must be contiguous")
+    return shape[0], shape[1], shape[3]
+
+
+def rope_frequencies(rotary_dim: int, theta: float = 1.0e4, *, scaling: Optional[str] = None,
+                     factor: float = 1.0, trained_len: int = 4096, slow_turns: float = 1.0,
+                     fast_turns: float = 32.0, device="cuda"):
+    """The angle per position of each rotated pair, float64[rotary_dim / 2],
+    and the factor of cosine and sine: the ``inv_freq`` and ``magnitude`` of
+    ``rope_append``.  Pair i turns by theta^(-2 i / rotary_dim) per position.
+
+    scaling stretches a model trained on ``trained_len`` positions by ``factor``:
+    None: not at all; "even": every angle divided by factor; "base": theta
+    raised so that the slowest pair is divided by factor and the fastest kept;
+    "parts": pairs that turn at least ``fast_turns`` times over trained_len
+    are kept, those that turn at most ``slow_turns`` times divided by factor,
+    those between blended linearly in their number of turns, with magnitude
+    0.1 ln(factor) + 1."""
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    if not (theta > 0 and factor >= 1.0):
+        raise ValueError("theta must be positive and factor at least 1")
+    n = rotary_dim // 2
+    magnitude = 1.0
+    if scaling == "base" and n > 1:
+        theta = theta * factor ** (rotary_dim / (rotary_dim - 2))
+    f = [theta ** (-2.0 * i / rotary_dim) for i in range(n)]
+    if scaling == "even":
+        f = [x / factor for x in f]
+    elif scaling == "parts":
+        if not fast_turns > slow_turns:
+            raise ValueError("fast_turns must exceed slow_turns")
+        keep = [min(1.0, max(0.0, (trained_len * x / (2.0 * math.pi) - slow_turns)
+                             / (fast_turns - slow_turns))) for x in f]
+        f = [x * k + x / factor * (1.0 - k) for x, k in zip(f, keep)]
+        magnitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError("scaling must be None, 'even', 'base' or 'parts'")
+    return torch.tensor(f, dtype=torch.float64, device=device), magnitude
+
+
+def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                positions: torch.Tensor, page_table: torch.Tensor, k_pool: torch.Tensor,
+                v_pool: torch.Tensor, inv_freq: torch.Tensor, *,
+                seq: Optional[torch.Tensor] = None, interleaved: bool = False,
+                magnitude: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                status: Optional[Status] = None, stream=None) -> Optional[torch.Tensor]:
+    """Rotate keys and append them with their values to one layer's paged
+    cache; rotate queries on the way (mk_rope_append).
+
+    q [tokens][query heads][hd] or None, k and v [tokens][kv heads][hd] (any
+    strides, columns adjacent) of float32, bfloat16 or float16; k_pool and
+    v_pool [pages][kv heads][64][hd] of bfloat16 or float16, written in place;
+    positions int32[tokens]; page_table int32[rows][pages per row]; seq
+    int32[tokens], each token's row (-1: padding, left out), or None: token t
+    is row t.  inv_freq float64[rotary_dim / 2] and magnitude as from
+    ``rope_frequencies``.  Returns q_out ([tokens][query heads][hd] of the
+    pools' type; allocated if None, may be q itself), None without queries."""
+    dev = _cuda(k, "k")
+    n_pages, hkv, hd = _pools(k_pool, v_pool, dev)
+    t = k.shape[0]
+    src = _TYPE.get(k.dtype)
+    if src is None or v.dtype != k.dtype or v.device != dev:
+        raise TypeError("k and v must have the same type (float32, bfloat16 or float16) and device")
+    if k.shape != (t, hkv, hd) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [tokens][{hkv}][{hd}]")
+    ks, vs = k.stride(), v.stride()
+    if t and (ks[2] != 1 or vs[2] != 1):
+        raise ValueError("the columns of k and v must be adjacent")
+    hq, qs = 0, (0, 0, 1)
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        if q.shape != (t, hq, hd) or hq < 1:
+            raise ValueError(f"q must be [tokens][query heads][{hd}]")
+        if q.dtype != k.dtype or q.device != dev:
+            raise TypeError("q must have the type and device of k")
+        qs = q.stride()
+        if t and qs[2] != 1:
+            raise ValueError("the columns of q must be adjacent")
+        if q_out is None:
+            q_out = torch.empty((t, hq, hd), dtype=k_pool.dtype, device=dev)
+        elif (q_out.shape != (t, hq, hd) or not q_out.is_contiguous()
+              or q_out.dtype != k_pool.dtype or q_out.device != dev):
+            raise ValueError("q_out must be contiguous, shaped like q and of the pools' type and device")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if inv_freq.dtype != torch.float64 or inv_freq.device != dev or not inv_freq.is_contiguous():
+        raise TypeError(f"inv_freq must be a contiguous float64 tensor on {dev}")
+    if inv_freq.dim() != 1 or 2 * inv_freq.numel() > hd:
+        raise ValueError(f"inv_freq must hold at most {hd // 2} frequencies")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [rows][pages per row]")
+    rows = page_table.shape[0]
+    if seq is None and t > rows:
+        raise ValueError("more tokens than page-table rows, and no seq")
+    a = mk.mk_rope_append_args(
+        dev.index, t, rows, page_table.shape[1], n_pages, hq, hkv, hd, 2 * inv_freq.numel(),
+        1 if interleaved else 0, src, _TYPE[k_pool.dtype], magnitude,
+        q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(),
+        qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+        q_out.data_ptr() if q is not None else None, k_pool.data_ptr(), v_pool.data_ptr(),
+        inv_freq.data_ptr(), _index(positions, "positions", dev, (t,)),
+        _index(seq, "seq", dev, (t,)) if seq is not None else None,
+        _index(page_table, "page_table", dev, page_table.shape), _status(status, dev))
+    if t:
+        mk.check_status(mk.lib.mk_rope_append(byref(a), _stream(stream, dev)), "mk_rope_append")
+    return q_out
+
+
+def prefix_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                     page_table: torch.Tensor, positions: torch.Tensor,
+                     group_start: torch.Tensor, prefix_lens: torch.Tensor, *,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, status: Optional[Status] = None,
+                     stream=None) -> torch.Tensor:
+    """Attention of one query token per batch entry over the paged cache,
+    shared prefixes read once per group (mk_prefix_attention).
+
+    q [batch][query heads][hd] of the pools' type; positions int32[batch]: entry
+    b attends to tokens 0 .. positions[b] of its sequence (-1: to none, output
+    zero); group g is entries group_start[g] .. group_start[g + 1] - 1, whose
+    first prefix_lens[g] tokens are read through the first entry's page-table
+    row; entries of no group keep their rows of out and lse.  A batch of one
+    sequence's tokens at increasing positions under a prefix that covers them
+    all is a causal piece of a prompt.  scale: factor of the scores, 1 /
+    sqrt(hd) by default.  Returns out (allocated if None: entries of no group
+    are then zero); lse, if given, float32[batch][query heads], receives the log
+    of each row's sum of exponentials."""
+    dev = _cuda(q, "q")
+    n_pages, hkv, hd = _pools(k_pool, v_pool, dev)
+    if q.dim() != 3 or q.shape[2] != hd:
+        raise ValueError(f"q must be [batch][query heads][{hd}]")
+    b, hq, _ = q.shape
+    if q.dtype != k_pool.dtype:
+        raise TypeError("q must have the pools' type")
+    qs = q.stride()
+    if b and (qs[2] != 1 or qs[1] != hd or qs[0] % 8):
+        raise ValueError("q's heads must be adjacent and its token stride a multiple of 8")
+    if hq < 1 or hq % hkv:
+        raise ValueError("query heads must be a multiple of the kv heads")
+    if page_table.dim() != 2 or group_start.dim() != 1 or prefix_lens.dim() != 1:
+        raise ValueError("page_table must be [batch][pages per row], group_start and prefix_lens flat")
+    n = prefix_lens.shape[0]
+    if out is None:
+        out = torch.zeros((b, hq, hd), dtype=q.dtype, device=dev)
+    elif (out.shape != (b, hq, hd) or not out.is_contiguous() or out.dtype != q.dtype
+          or out.device != dev):
+        raise ValueError("out must be contiguous with q's shape, type and device")
+    a = mk.mk_prefix_attention_args(
+        dev.index, b, n, page_table.shape[1], n_pages, hq, hkv, hd, _TYPE[q.dtype],
+        scale if scale is not None else 1.0 / math.sqrt(hd), q.data_ptr(), qs[0],
+        k_pool.data_ptr(), v_pool.data_ptr(),
+        _index(page_table, "page_table", dev, (b, page_table.shape[1])),
+        _index(positions, "positions", dev, (b,)),
+        _index(group_start, "group_start", dev, (n + 1,)),
+        _index(prefix_lens, "prefix_lens", dev, (n,)), out.data_ptr(),
+        _float(lse, "lse", dev, (b, hq)) if lse is not None else None, None, 0,
+        _status(status, dev))
+    if b == 0 or n == 0:
+        return out
+    size = mk.lib.mk_prefix_attention_workspace(byref(a))
+    # the workspace is this call's own; torch hands its memory on in stream order
+    if stream is None:
+        work = torch.empty(size, dtype=torch.uint8, device=dev)
+    else:
+        with torch.cuda.stream(stream):
+            work = torch.empty(size, dtype=torch.uint8, device=dev)
+    a.workspace, a.workspace_bytes = work.data_ptr(), size
+    mk.check_status(mk.lib.mk_prefix_attention(byref(a), _stream(stream, dev)),
+                    "mk_prefix_attention")
+    return out
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch.Tensor] = None,
+           top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+           min_p: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+           logprobs: Optional[torch.Tensor] = None, status: Optional[Status] = None,
+           stream=None) -> torch.Tensor:
+    """Draw one token per row of logits from given uniform numbers (mk_sample).
+
+    logits [batch][vocab] of float32, bfloat16 or float16 (columns adjacent);
+    u float32[batch] in [0, 1).  temperature, top_p, min_p float32[batch] and
+    top_k int32[batch] are each optional.  The kept tokens are those of the
+    top_k largest logits whose preceding probability, among these, is below
+    top_p, and whose probability is at least min_p of the largest; the drawn
+    one is the first, by ascending id, at which their running probability
+    passes u.  temperature 0 picks the largest logit.  Returns tokens
+    int32[batch] (allocated if None; -1 where a row has nothing to draw);
+    logprobs, if given, float32[batch], receives each drawn token's log-probability
+    among the kept ones."""
+    dev = _cuda(logits, "logits")
+    kind = _TYPE.get(logits.dtype)
+    if kind is None:
+        raise TypeError("logits must be float32, bfloat16 or float16")
+    if logits.dim() != 2 or logits.shape[1] < 1:
+        raise ValueError("logits must be [batch][vocab]")
+    b, v = logits.shape
+    ls = logits.stride()
+    if b and ls[1] != 1 and v > 1:
+        raise ValueError("the columns of logits must be adjacent")
+    rows = (b,)
+    if tokens is None:
+        tokens = torch.empty(b, dtype=_I32, device=dev)
+    a = mk.mk_sample_args(
+        dev.index, b, v, kind, logits.data_ptr(), ls[0], _float(u, "u", dev, rows),
+        _float(temperature, "temperature", dev, rows) if temperature is not None else None,
+        _index(top_k, "top_k", dev, rows) if top_k is not None else None,
+        _float(top_p, "top_p", dev, rows) if top_p is not None else None,
+        _float(min_p, "min_p", dev, rows) if min_p is not None else None,
+        _index(tokens, "tokens", dev, rows),
+        _float(logprobs, "logprobs", dev, rows) if logprobs is not None else None,
+        _status(status, dev))
+    if b:
+        mk.check_status(mk.lib.mk_sample(byref(a), _stream(stream, dev)), "mk_sample")
+    return tokens
