@@ -441,7 +441,7 @@ mk_status mk_prefix_attention(const mk_prefix_attention_args* args, void* stream
  * temperature is negative or not finite, whose u is outside [0, 1), or whose
  * top_p or min_p is NaN: a device-side fault.
  * vocab is at most MK_SAMPLE_MAX_VOCAB.                                     */
-#define MK_SAMPLE_MAX_VOCAB 409600
+#define MK_SAMPLE_MAX_VOCAB 368640
 typedef struct mk_sample_args {
   int32_t device;
   int32_t batch, vocab;

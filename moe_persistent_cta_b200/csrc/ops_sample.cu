@@ -13,7 +13,16 @@
 // taken in a fixed order, so a call gives the same tokens every time.
 //
 // Bound: one read of the logits.  A cluster of up to 8 blocks holds a row in
-// its shared memory, so the passes below touch memory once.
+// its shared memory, so the passes below touch memory once.  The cut is found
+// by one of three ways:
+//  * top_k up to 64 x blocks: the k-th largest of the maxima of as many groups
+//    of tokens is a logit that at least k tokens reach, and hardly more than
+//    k; those are gathered in one block and sorted, which settles everything.
+//  * top_p alone: a histogram of the distance to the largest logit brackets
+//    the weight of the tokens down to each bin within 1e-5, so the cut lies in
+//    one bin or two; their tokens are gathered and sorted.
+//  * otherwise (large top_k, very many equal logits): the range of keys is
+//    split in four, again and again, by exact sums.
 #include <cooperative_groups.h>
 
 #include "ops_common.cuh"
@@ -28,6 +37,9 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kList = 2048;          // tokens that can be gathered and sorted
+constexpr int kBins = 2048;          // histogram of the distance to the largest
+constexpr int kGroups = kThreads / 8;   // groups of a block whose maxima are kept
 
 struct SampleParams {
   int B, V;
@@ -75,12 +87,47 @@ struct Exchange {
 };
 
 struct Shared {
+  unsigned long long list[kList];    // gathered tokens, (key << 32) | ~id
+  union {
+    struct {
+      uint32_t count[kBins];         // tokens of a bin
+      uint32_t part[kBins];          // sum of their places in it, in 1/256ths
+    } hist;
+    struct {
+      double w[kThreads];            // the draw among sorted tokens
+      int id[kThreads];
+    } draw;
+  };
+  double exp2_tab[256];              // 2^(j / 256)
+  uint32_t group_max[kMaxCluster * kGroups];
   double warp_val[kWarps][3];
   unsigned long long warp_key[kWarps];
   Exchange ex;
-  double total[3];
-  unsigned long long key;
-  unsigned int first;        // first thread past the target
+  uint32_t cut, cut_id;              // handed round by the sorting block
+  int n_list, first_bin, last_bin, picked;
+};
+
+// exp(z) for z = d / T <= 0, d = x - max: with y = d (256 / ln 2) / T = n + r,
+// |r| <= 1/2, it is 2^(n / 256) exp(r ln 2 / 256): a table of 256 values and a
+// polynomial of degree 4, whose remainder is below 2^-54 (Tang's table-driven
+// method).  10 64-bit operations; the library's exp takes about twice as many
+// and bounded the passes over a row.
+struct Weight {
+  const double* tab;
+  double mx, k;                      // largest logit, (256 / ln 2) / T
+  __device__ __forceinline__ double operator()(float x) const {
+    constexpr double kMagic = 6755399441055744.0;          // 1.5 x 2^52: rounds to an integer
+    constexpr double c1 = 0.0027076061740622863;           // ln 2 / 256
+    constexpr double c2 = c1 * c1 / 2, c3 = c1 * c1 * c1 / 6, c4 = c1 * c1 * c1 * c1 / 24;
+    const double y = fmax(((double)x - mx) * k, -300000.0);
+    const double t = y + kMagic;
+    const int n = __double2loint(t);
+    const double r = y - (t - kMagic);
+    const double v = tab[n & 255];
+    const double w = fma(v * r, fma(r, fma(r, fma(r, c4, c3), c2), c1), v);
+    const int e = n >> 8;
+    return e < -1021 ? 0.0 : __hiloint2double(__double2hiint(w) + (e << 20), __double2loint(w));
+  }
 };
 
 // A row's state, the same in every thread of the cluster.
@@ -91,14 +138,18 @@ struct Row {
   int id0;               // id of the first
   int lo, hi;            // this thread's range of them
   float mx;
-  double inv_t;
+  Weight exp_of;
   bool inf;              // the largest logit is +infinity
 
   __device__ __forceinline__ double weight(float x) const {
     if (inf) return x == INFINITY ? 1.0 : 0.0;
-    return exp(((double)x - (double)mx) * inv_t);
+    return exp_of(x);
   }
 };
+
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
 
 class Cluster {
  public:
@@ -167,11 +218,21 @@ class Cluster {
       cg::this_cluster().sync();
   }
 
- private:
   template <typename U>
   __device__ U* remote(U* p, int r) {
     return size_ == 1 ? p : cg::this_cluster().map_shared_rank(p, r);
   }
+  // A barrier in two parts: every block of the cluster has begun.
+  __device__ void arrive() {
+    if (size_ > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  }
+  __device__ void wait() {
+    if (size_ > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  __device__ int size() const { return size_; }
+  __device__ int rank() const { return rank_; }
+
+ private:
 
   Shared* s_;
   int rank_, size_;
@@ -263,17 +324,251 @@ __device__ uint32_t nth_equal(Cluster& cl, Shared* s, const Row<T>& row, uint32_
   return (uint32_t)(cl.max_key(found) - 1ull);
 }
 
+// Sorts s->list[0 .. n) in descending order (n <= kList); ends with a barrier.
+// Bitonic; steps whose pairs lie within 64 entries stay inside a warp.
+__device__ void sort_list(Shared* s, int n) {
+  int size = 64;
+  while (size < n) size *= 2;
+  for (int i = n + threadIdx.x; i < size; i += kThreads) s->list[i] = 0;
+  __syncthreads();
+  for (int k = 2; k <= size; k *= 2) {
+    for (int j = k / 2; j > 0; j /= 2) {
+      for (int q = threadIdx.x; q < size / 2; q += kThreads) {
+        const int a = 2 * q - (q & (j - 1)), b = a + j;
+        const unsigned long long x = s->list[a], y = s->list[b];
+        if ((x < y) == ((a & k) == 0)) {
+          s->list[a] = y;
+          s->list[b] = x;
+        }
+      }
+      if (j > 32 || (j == 1 && k >= 64))
+        __syncthreads();
+      else
+        __syncwarp();
+    }
+  }
+  __syncthreads();
+}
+
+// Appends this block's tokens that `want` picks to its list, kList at most;
+// n_list counts all.  Ends with a barrier.
+template <typename T, typename F>
+__device__ void gather(Shared* s, const Row<T>& row, F want) {
+  if (threadIdx.x == 0) s->n_list = 0;
+  __syncthreads();
+  for (int i = row.lo; i < row.hi; ++i) {
+    const float x = to_float(row.vals[i]);
+    if (want(x)) {
+      const int at = atomicAdd(&s->n_list, 1);
+      if (at < kList)
+        s->list[at] = ((unsigned long long)key_of(x) << 32) | (uint32_t)~(uint32_t)(row.id0 + i);
+    }
+  }
+  __syncthreads();
+}
+
+// Collects the lists of all blocks, behind a cluster barrier, in block 0,
+// sorted there.  Returns how many tokens there are; if more than kList, nothing
+// is collected.  After its own cluster barrier block 0 reads no other's memory.
+__device__ int collect(Cluster& cl, Shared* s) {
+  int total = 0, base = 0;
+  for (int r = 0; r < cl.size(); ++r) {
+    const int n = *cl.remote(&s->n_list, r);
+    total += n;
+  }
+  if (total <= kList && cl.rank() == 0) {
+    base = s->n_list;
+    for (int r = 1; r < cl.size(); ++r) {
+      const int n = *cl.remote(&s->n_list, r);
+      const unsigned long long* src = cl.remote(s->list, r);
+      for (int i = threadIdx.x; i < n; i += kThreads) s->list[base + i] = src[i];
+      base += n;
+    }
+  }
+  cl.sync();
+  if (total <= kList && cl.rank() == 0) sort_list(s, total);
+  return total;
+}
+
+// Sorted tokens of a thread: four consecutive ones.
+constexpr int kEach = kList / kThreads;
+
+// Block 0, with the list sorted: how many of the first n tokens are kept by
+// a limit on the sum before each, starting from `above`: `target`, or top_p of
+// the n tokens' sum where target is negative.  *all: the sum behind them.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, int cluster) {
+__device__ int keep_sorted(Shared* s, const Row<T>& row, int n, float top_p, double above, double target,
+                           double* all) {
+  double w[kEach], mine = 0.0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = kEach * (int)threadIdx.x + e;
+    w[e] = i < n ? row.weight(value_of((uint32_t)(s->list[i] >> 32))) : 0.0;
+    mine += w[e];
+  }
+  double before = above + below_in_block(s, mine);
+  if (threadIdx.x == kThreads - 1) s->warp_val[0][1] = before + mine;
+  if (threadIdx.x == 0) s->n_list = 0;
+  __syncthreads();
+  *all = s->warp_val[0][1];
+  if (target < 0.0) target = (double)top_p * *all;
+  int keep = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = kEach * (int)threadIdx.x + e;
+    keep += i < n && (top_p >= 1.0f || before < target);
+    before += w[e];
+  }
+  // what is kept is a prefix, so the number says which
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) keep += __shfl_xor_sync(kFull, keep, o);
+  if ((threadIdx.x & 31) == 0 && keep) atomicAdd(&s->n_list, keep);
+  __syncthreads();
+  return s->n_list;
+}
+
+// The draw among the first `keep` (1 .. kThreads) tokens of the sorted list, one
+// per thread: each one's running sum over the ids up to its own, added in the
+// order of the list.  True in the thread that holds the drawn token.
+template <typename T>
+__device__ bool draw_sorted(Shared* s, const Row<T>& row, int keep, float min_p, float u, int* token,
+                            float* logprob) {
+  const bool have = (int)threadIdx.x < keep;
+  double w = 0.0;
+  int id = 0x7fffffff;
+  if (have) {
+    const unsigned long long e = s->list[threadIdx.x];
+    w = row.weight(value_of((uint32_t)(e >> 32)));
+    if (threadIdx.x > 0 && w < (double)min_p) w = 0.0;
+    id = (int)~(uint32_t)e;
+  }
+  s->draw.w[threadIdx.x] = w;
+  s->draw.id[threadIdx.x] = id;
+  if (threadIdx.x == 0) s->picked = 0x7fffffff;
+  __syncthreads();
+  double upto = 0.0, z = 0.0;
+#pragma unroll 4
+  for (int j = 0; j < keep; ++j) {
+    const double wj = s->draw.w[j];
+    z += wj;
+    if (s->draw.id[j] <= id) upto += wj;
+  }
+  if (have && w > 0.0 && upto > (double)u * z) atomicMin(&s->picked, id);
+  __syncthreads();
+  if (s->picked == 0x7fffffff) {     // by rounding: the last one, then
+    __syncthreads();
+    if (threadIdx.x == 0) s->picked = -1;
+    __syncthreads();
+    if (have && w > 0.0) atomicMax(&s->picked, id);
+    __syncthreads();
+  }
+  if (!have || id != s->picked) return false;
+  *token = id;
+  *logprob = (float)log(w / z);
+  return true;
+}
+
+// The cut of top_p over all tokens, by the histogram.  False if it has to be
+// found another way (the same in every thread of the cluster).
+template <typename T>
+__device__ bool cut_by_bins(Cluster& cl, Shared* s, const Row<T>& row, int V, float top_p, float temp,
+                            uint32_t* cut, uint32_t* cut_id) {
+  // Tokens further than `reach` below the largest (in exponents) weigh less than
+  // V exp(-reach) = (1 - top_p) / e of it together: the cut is not among them.
+  const float reach = logf((float)V / (1.0f - top_p)) + 1.0f;
+  const float scale = (float)kBins / (reach * temp), step = reach / (float)kBins;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) s->hist.count[i] = s->hist.part[i] = 0;
+  __syncthreads();
+  double sum = 0.0;
+  for (int i = row.lo; i < row.hi; ++i) {
+    const float x = to_float(row.vals[i]);
+    const float place = (row.mx - x) * scale;
+    if (place < (float)kBins) {
+      const int bin = (int)place;
+      atomicAdd(&s->hist.count[bin], 1u);
+      atomicAdd(&s->hist.part[bin], (uint32_t)((place - (float)bin) * 256.0f));
+    }
+    sum += row.weight(x);
+  }
+  double t[3];
+  cl.sum3(sum, 0.0, 0.0, t);
+  const double target = (double)top_p * t[0];
+  // A bin's weight lies between n exp(-mean) and that times 1 + step^2 / 8; the
+  // mean is known to 1/256 of a bin; places are rounded to 2^-12 of one.
+  const double slack = (double)step * (1.0 / 256 + step / 8 + 1.0 / 4096) + 1e-6;
+  constexpr int kOwn = kBins / kThreads;
+  uint32_t count[kOwn] = {}, part[kOwn] = {};
+  static_assert(kOwn == 4, "one 16-byte load per block");
+  for (int r = 0; r < cl.size(); ++r) {
+    const uint4 c = reinterpret_cast<const uint4*>(cl.remote(s->hist.count, r))[threadIdx.x];
+    const uint4 q = reinterpret_cast<const uint4*>(cl.remote(s->hist.part, r))[threadIdx.x];
+    count[0] += c.x; count[1] += c.y; count[2] += c.z; count[3] += c.w;
+    part[0] += q.x; part[1] += q.y; part[2] += q.z; part[3] += q.w;
+  }
+  double upto[kOwn], mine = 0.0;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const float mean = count[i] ? (float)part[i] / (256.0f * (float)count[i]) : 0.0f;
+    mine += (double)count[i] * exp(-(double)step * ((double)(kOwn * threadIdx.x + i) + (double)mean));
+    upto[i] = mine;
+  }
+  if (threadIdx.x == 0) s->first_bin = s->last_bin = kBins;
+  const double below = below_in_block(s, mine);
+#pragma unroll
+  for (int i = kOwn - 1; i >= 0; --i) {
+    const int bin = kOwn * threadIdx.x + i;
+    if ((below + upto[i]) * (1.0 + slack) >= target) atomicMin(&s->first_bin, bin);
+    if ((below + upto[i]) * (1.0 - slack) >= target) atomicMin(&s->last_bin, bin);
+  }
+  __syncthreads();
+  const int first = s->first_bin, last = s->last_bin;
+  if (last >= kBins) return false;
+  if (threadIdx.x == 0) s->n_list = 0;
+  __syncthreads();
+  double above = 0.0;
+  for (int i = row.lo; i < row.hi; ++i) {
+    const float x = to_float(row.vals[i]);
+    const float place = (row.mx - x) * scale;
+    if (!(place < (float)(last + 1))) continue;
+    if (place < (float)first) {
+      above += row.weight(x);
+    } else {
+      const int at = atomicAdd(&s->n_list, 1);
+      if (at < kList)
+        s->list[at] = ((unsigned long long)key_of(x) << 32) | (uint32_t)~(uint32_t)(row.id0 + i);
+    }
+  }
+  cl.sum3(above, 0.0, 0.0, t);       // behind its barriers every list is whole
+  const int n = collect(cl, s);
+  if (n > kList) return false;
+  if (cl.rank() == 0) {
+    double all;
+    const int keep = keep_sorted(s, row, n, top_p, t[0], target, &all);
+    if ((int)threadIdx.x < cl.size()) {
+      // the cut has to lie among these tokens
+      const bool found = keep > 0 && (keep < n || all >= target);
+      const unsigned long long e = found ? s->list[keep - 1] : 0ull;
+      *cl.remote(&s->cut, threadIdx.x) = (uint32_t)(e >> 32);
+      *cl.remote(&s->cut_id, threadIdx.x) = (uint32_t)~(uint32_t)e;
+    }
+  }
+  cl.sync();
+  if (s->cut == 0) return false;
+  *cut = s->cut;
+  *cut_id = s->cut_id;
+  return true;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p, int cluster) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   __shared__ Shared s;
   const int rank = cluster == 1 ? 0 : (int)cg::this_cluster().block_rank();
   const int b = blockIdx.x / cluster;
   Cluster cl(&s, rank, cluster);
-  T* vals = reinterpret_cast<T*>(s_raw);
+  cl.arrive();
 
   Row<T> row;
-  row.vals = vals;
   row.id0 = rank * kThreads * p.per;
   row.n = max(0, min(p.V - row.id0, kThreads * p.per));
   row.lo = min(row.n, (int)threadIdx.x * p.per);
@@ -285,18 +580,62 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
   const float top_p = p.top_p ? __ldg(p.top_p + b) : 1.0f;
   const float min_p = p.min_p ? __ldg(p.min_p + b) : 0.0f;
 
-  // the row's part into shared memory; the largest logit, at its lowest id
+  // the row's part into shared memory, at the same place within 16 bytes as in
+  // global memory; the largest logit, at its lowest id
   const T* src = static_cast<const T*>(p.logits) + (size_t)b * p.stride + row.id0;
-  unsigned long long best = 0;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < row.n; i += kThreads) {
-    const T x = store_clean<T>(src[i]);
-    vals[i] = x;
-    const unsigned long long c =
-        ((unsigned long long)key_of(to_float(x)) << 32) | (uint32_t)~(uint32_t)(row.id0 + i);
-    best = c > best ? c : best;
+  const int shift = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+  T* vals = reinterpret_cast<T*>(s_raw + shift);
+  row.vals = vals;
+  uint32_t top = 0;                  // this thread's largest key and its id
+  int top_id = 0;
+  auto take = [&](T v, int i) {
+    const T x = store_clean<T>(v);
+    const uint32_t key = key_of(to_float(x));
+    if (key > top) {                 // ids ascend: the first of equal ones stays
+      top = key;
+      top_id = row.id0 + i;
+    }
+    return x;
+  };
+  constexpr int VE = 16 / sizeof(T);
+  const int lead = min(row.n, ((16 - shift) & 15) / (int)sizeof(T));
+  const int vecs = (row.n - lead) / VE;
+  if ((int)threadIdx.x < lead) vals[threadIdx.x] = take(src[threadIdx.x], threadIdx.x);
+  {
+    const uint4* from = reinterpret_cast<const uint4*>(src + lead);
+    uint4* to = reinterpret_cast<uint4*>(vals + lead);
+    constexpr int kAhead = 8;
+    for (int i0 = threadIdx.x; i0 < vecs; i0 += kAhead * kThreads) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        if (i0 + a * kThreads < vecs) v[a] = __ldcs(from + i0 + a * kThreads);
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int i = i0 + a * kThreads;
+        if (i < vecs) {
+          T* e = reinterpret_cast<T*>(&v[a]);
+#pragma unroll
+          for (int c = 0; c < VE; ++c) e[c] = take(e[c], lead + i * VE + c);
+          to[i] = v[a];
+        }
+      }
+    }
   }
-  best = cl.max_key(best);           // also: every block's part is written
+  for (int i = lead + vecs * VE + threadIdx.x; i < row.n; i += kThreads) vals[i] = take(src[i], i);
+  if (threadIdx.x < 256) s.exp2_tab[threadIdx.x] = exp2((double)threadIdx.x / 256.0);
+  {
+    uint32_t g = top;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(kFull, g, o));
+    cl.wait();                       // every block runs: its memory may be written
+    if ((threadIdx.x & 7) == 0)
+      for (int r = 0; r < cluster; ++r)
+        *cl.remote(&s.group_max[rank * kGroups + threadIdx.x / 8], r) = g;
+  }
+  // also: every block's part, table and maxima are written
+  const unsigned long long best =
+      cl.max_key(((unsigned long long)top << 32) | (uint32_t)~(uint32_t)top_id);
   const uint32_t max_k = (uint32_t)(best >> 32);
   const int max_id = (int)~(uint32_t)best;
 
@@ -310,94 +649,132 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
       report(p.status, MK_ERR_DEVICE, MK_OP_SAMPLE, b, __float_as_int(!(u >= 0.0f && u < 1.0f) ? u : temp), 0);
   } else if (max_k <= kKeyMinusInf) {
     // nothing to draw
-  } else if (temp == 0.0f) {
-    token = max_id;
+  } else if (temp == 0.0f || top_p <= 0.0f || k == 1 || min_p > 1.0f) {
+    token = max_id;                  // nothing else is kept
     logprob = 0.0f;
   } else {
-    const uint32_t mb = (max_k & 0x80000000u) ? (max_k & 0x7fffffffu) : ~max_k;
-    row.mx = __uint_as_float(mb);
+    row.mx = value_of(max_k);
     row.inf = row.mx == INFINITY;
-    row.inv_t = 1.0 / (double)temp;
+    row.exp_of = Weight{s.exp2_tab, (double)row.mx, 369.32993046757463 / (double)temp};
     const uint32_t floor_key = row.inf ? max_k : kKeyMinusInf + 1;
     // the cut: tokens with a larger key, or an equal one and id <= cut_id
     uint32_t cut = floor_key, cut_id = 0xffffffffu;
-    double whole = -1.0;             // the first top_k tokens' sum, where needed
+    bool settled = false;            // block 0 has drawn among the gathered tokens
     double t[3];
-    if (k > 0 && k < p.V) {
+    const bool limited = k > 0 && k < p.V;
+    if (limited && k <= kThreads && (k <= cluster * kGroups || p.V <= kList)) {
+      // the k-th largest of the groups' maxima to 20 bits, rounded down: k
+      // tokens or more reach it.  A small vocabulary is gathered whole.
+      uint32_t t0 = 0;
+      if (p.V > kList) {
+        const uint32_t mine = (int)threadIdx.x < cluster * kGroups ? s.group_max[threadIdx.x] : 0;
+        for (int bit = 31; bit >= 12; --bit) {
+          const uint32_t c = t0 | (1u << bit);
+          if (__syncthreads_count(mine >= c) >= k) t0 = c;
+        }
+      }
+      t0 = max(t0, floor_key);
+      gather(&s, row, [&](float x) { return key_of(x) >= t0; });
+      cl.sync();
+      const int n = collect(cl, &s);
+      if (n <= kList) {
+        settled = true;
+        writer = false;
+        if (rank == 0) {
+          double all;
+          const int keep = keep_sorted(&s, row, min(n, k), top_p, 0.0, -1.0, &all);
+          writer = draw_sorted(&s, row, max(keep, 1), min_p, u, &token, &logprob);
+        }
+      }
+    }
+    if (limited && !settled) {
       double above, at;
       cut = find_cut<true>(cl, row, floor_key, (double)k, &above, &at);
       if (above + at > (double)k) cut_id = nth_equal(cl, &s, row, cut, (double)k - above);
     }
-    auto kept = [&](float x, int id) {
-      const uint32_t key = key_of(x);
-      return key > cut || (key == cut && (uint32_t)id <= cut_id);
-    };
-    if (top_p < 1.0f) {
-      double sum = 0.0;
+    if (!settled) {
+      auto kept = [&](float x, int id) {
+        const uint32_t key = key_of(x);
+        return key > cut || (key == cut && (uint32_t)id <= cut_id);
+      };
+      if (top_p < 1.0f && (limited || row.inf || !cut_by_bins(cl, &s, row, p.V, top_p, temp, &cut, &cut_id))) {
+        double sum = 0.0;
+        for (int i = row.lo; i < row.hi; ++i) {
+          const float x = to_float(vals[i]);
+          if (kept(x, row.id0 + i)) sum += row.weight(x);
+        }
+        cl.sum3(sum, 0.0, 0.0, t);
+        const double target = (double)top_p * t[0];
+        double above, at;
+        const uint32_t c = find_cut<false>(cl, row, cut, target, &above, &at);
+        if (c > cut || (c == cut && above < target)) {
+          // of the equal tokens at the cut, as many as reach the target
+          const double w = row.weight(value_of(c));
+          double need = w > 0.0 ? ceil((target - above) / w) : 1.0;
+          if (need < 1.0) need = 1.0;
+          const double have = w > 0.0 ? rint(at / w) : 1.0;
+          if (need < have) {
+            const uint32_t id = nth_equal(cl, &s, row, c, need);
+            cut_id = c == cut ? min(cut_id, id) : id;
+          } else if (c > cut) {
+            cut_id = 0xffffffffu;
+          }
+          cut = c;
+        }
+      }
+      if (min_p > 0.0f && !row.inf) {
+        // what is surely below min_p needs no weight: min_p's logit, lowered by
+        // more than its rounding
+        const double x = (double)row.mx + (double)temp * log((double)min_p);
+        const double low = x - 1e-6 * (fabs(x) + fabs((double)row.mx));
+        if (low > -3e38) {
+          const uint32_t c = key_of((float)low + 0.0f);
+          if (c > cut) {
+            cut = c;
+            cut_id = 0xffffffffu;
+          }
+        }
+      }
+      // the draw, in id order
+      double mine = 0.0;
+      int last = -1;
       for (int i = row.lo; i < row.hi; ++i) {
         const float x = to_float(vals[i]);
-        if (kept(x, row.id0 + i)) sum += row.weight(x);
-      }
-      cl.sum3(sum, 0.0, 0.0, t);
-      whole = t[0];
-      const double target = (double)top_p * whole;
-      double above, at;
-      const uint32_t c = find_cut<false>(cl, row, cut, target, &above, &at);
-      if (c > cut || (c == cut && above < target)) {
-        // of the equal tokens at the cut, as many as reach the target
-        const uint32_t cb = (c & 0x80000000u) ? (c & 0x7fffffffu) : ~c;
-        const double w = row.weight(__uint_as_float(cb));
-        double need = w > 0.0 ? ceil((target - above) / w) : 1.0;
-        if (need < 1.0) need = 1.0;
-        const double have = w > 0.0 ? rint(at / w) : 1.0;
-        if (need < have) {
-          const uint32_t id = nth_equal(cl, &s, row, c, need);
-          cut_id = c == cut ? min(cut_id, id) : id;
-        } else if (c > cut) {
-          cut_id = 0xffffffffu;
-        }
-        cut = c;
-      }
-    }
-    // the draw, in id order
-    double mine = 0.0;
-    int last = -1;
-    for (int i = row.lo; i < row.hi; ++i) {
-      const float x = to_float(vals[i]);
-      if (!kept(x, row.id0 + i)) continue;
-      const double w = row.weight(x);
-      if (w < (double)min_p || w == 0.0) continue;
-      mine += w;
-      last = i;
-    }
-    double under[3];
-    cl.sum3(mine, 0.0, 0.0, t, under);
-    const double z = t[0], target = (double)u * z;
-    const double before = under[0] + below_in_block(&s, mine);
-    // the first thread that holds kept tokens and passes the target; by
-    // rounding there may be none, then the last that holds any
-    const uint32_t place = (uint32_t)(rank * kThreads + threadIdx.x);
-    unsigned long long c = 0;
-    if (last >= 0)
-      c = before + mine > target ? (1ull << 62) - place : 1ull + place;
-    const unsigned long long won = cl.max_key(c);
-    writer = last >= 0 && c == won;
-    if (writer) {
-      double acc = before, w = 0.0;
-      int pick = last;
-      for (int i = row.lo; i <= last; ++i) {
-        const float x = to_float(vals[i]);
         if (!kept(x, row.id0 + i)) continue;
-        w = row.weight(x);
+        const double w = row.weight(x);
         if (w < (double)min_p || w == 0.0) continue;
-        acc += w;
-        if (acc > target) {
-          pick = i;
-          break;
-        }
+        mine += w;
+        last = i;
       }
-      token = row.id0 + pick;
-      logprob = (float)log(row.weight(to_float(vals[pick])) / z);
+      double under[3];
+      cl.sum3(mine, 0.0, 0.0, t, under);
+      const double z = t[0], target = (double)u * z;
+      const double before = under[0] + below_in_block(&s, mine);
+      // the first thread that holds kept tokens and passes the target; by
+      // rounding there may be none, then the last that holds any
+      const uint32_t place = (uint32_t)(rank * kThreads + threadIdx.x);
+      unsigned long long c = 0;
+      if (last >= 0)
+        c = before + mine > target ? (1ull << 62) - place : 1ull + place;
+      const unsigned long long won = cl.max_key(c);
+      writer = last >= 0 && c == won;
+      if (writer) {
+        double acc = before;
+        int pick = last;
+        for (int i = row.lo; i <= last; ++i) {
+          const float x = to_float(vals[i]);
+          if (!kept(x, row.id0 + i)) continue;
+          const double w = row.weight(x);
+          if (w < (double)min_p || w == 0.0) continue;
+          acc += w;
+          if (acc > target) {
+            pick = i;
+            break;
+          }
+        }
+        token = row.id0 + pick;
+        logprob = (float)log(row.weight(to_float(vals[pick])) / z);
+      }
     }
   }
   if (writer) {
@@ -410,7 +787,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
       if (p.seq_len != p.position) p.seq_len[b] += 1;
     }
   }
-  cl.sync();                         // no block leaves while another may write to it
+  // No barrier: behind the last one no block touches another's memory.
 }
 
 // Blocks a row is spread over and consecutive tokens of a thread.  The part a
@@ -427,12 +804,12 @@ cudaError_t launch_sample(const SampleParams& p0, cudaStream_t stream) {
   SampleParams p = p0;
   const int c = cluster_for(p.V);
   p.per = ((p.V + c * kThreads - 1) / (c * kThreads)) | 1;
-  const size_t smem = (size_t)p.per * kThreads * sizeof(T);
-  static_assert((MK_SAMPLE_MAX_VOCAB / (kMaxCluster * kThreads) + 1) * kThreads * 4 +
+  const size_t smem = (size_t)p.per * kThreads * sizeof(T) + 16;
+  static_assert((MK_SAMPLE_MAX_VOCAB / (kMaxCluster * kThreads) + 1) * kThreads * 4 + 16 +
                         sizeof(Shared) <= 227 * 1024,
                 "the largest vocabulary does not fit the cluster's shared memory");
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024)
+  if (smem > 8 * 1024)               // with Shared more than the default 48 KB
     e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem);
   if (e != cudaSuccess) return e;

@@ -24,7 +24,7 @@ MK_STATIC_SCRATCH_MAX_BYTES = 32 * 1024 * 1024
 TRACE_WORDS = 18
 MK_FP32, MK_BF16, MK_FP16 = 0, 1, 2
 MK_OP_ROPE_APPEND, MK_OP_PREFIX_ATTENTION, MK_OP_SAMPLE = 1, 2, 3
-MK_SAMPLE_MAX_VOCAB = 409600
+MK_SAMPLE_MAX_VOCAB = 368640
 
 # every entry point the header declares (checked by the ABI test)
 EXPORTS = (
