@@ -9,22 +9,31 @@
 // Any m not far below the largest score serves, so O is only rescaled when a
 // row's largest score has grown by more than 8 (a factor of 256).
 //
-// Work.  A unit is one KV head's query rows against one token range: the
-// prefix of up to 2 x floor(128 / G) entries of a group (G query heads per KV
-// head), or one entry's own tokens.  Units are cut into tiles; the tiles of
-// all units form one line, and every block takes an equal stretch of it, so a
-// long prefix is split over many blocks and short remainders share one.  Each
-// block finds its stretch from the device arrays: the host needs no lengths,
-// and a captured graph replays with new ones.  A block's share of a unit
-// leaves a partial result (O, m, l); a second launch adds them up.
+// Work.  Query rows are (entry, query head of one KV head).  Prefix units: one
+// KV head's rows of up to 2 x MB entries of a group (MB = floor(128 / G), G
+// query heads per KV head) against the group's prefix.  Own units: one entry's
+// rows against its own tokens; the entries of a chunk (MB consecutive ones)
+// share one tile of query rows, and one after another meet their tokens with
+// the other entries' rows masked, so that a block works through many short
+// remainders without a break.  The tiles of all units form one line, measured
+// in steps (one 128 x 128 S tile; a prefix tile that serves two tiles of rows
+// is two); every block takes an equal stretch of it.  Each block finds its
+// stretch from the device arrays: the host needs no lengths, and a captured
+// graph replays with new ones.  A block's share of a unit leaves partial
+// results (O, m, l); a second launch adds them up.
 //
 // One block: a TMA warp streams K and V tiles, a warp issues tcgen05 MMAs,
 // and two groups of four warps hold a softmax row per thread.  S = Q K^T and O
 // live in tensor memory, two of each ("streams"), so that one stream's softmax
 // runs under the other's MMAs.  With more than 128 rows the streams are the
-// two halves of the rows, and each K and V tile serves both; with fewer they
-// are alternate tiles of the same rows, joined at the end.  P goes back to
-// tensor memory over S and is the A operand of P V.
+// two tiles of rows, and each K and V tile serves both; with fewer they are
+// alternate tiles of tokens of the same rows, two partial results.  P goes
+// back to tensor memory over S and is the A operand of P V.
+//
+// Values that are no numbers.  A masked weight is 0, and 0 x infinity is NaN:
+// V's rows outside a unit's tokens are cleared in shared memory, but a row can
+// also meet tokens that only other rows of its tile see.  A row whose sum is
+// not finite is therefore computed once more, from its own tokens alone.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -42,65 +51,71 @@ constexpr int kGroupThreads = 128;   // a softmax group: one row per thread
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 320;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxSegments = 24;     // of one pass of a block over its stretch
+constexpr int kMaxItems = 48;        // of one pass of a block over its stretch
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroup = 64;        // query heads per KV head
 constexpr float kRescale = 8.0f;     // log2 of the growth that O may lag behind
 constexpr uint32_t kFull = 0xffffffffu;
-// Tiles of one unit cost alike, whatever their rows, while memory is the bound.
 constexpr int kWaitCycles = 1 << 30; // about half a second at any clock
+
+// What the joining launch needs of an entry, written by block 0: the places
+// in the line of its unit's first prefix tile and of its first own tile for KV
+// head 0, how far the next head's are, and how many tiles there are.
+struct __align__(16) Entry {
+  int prefix_at, prefix_tiles, prefix_width;   // steps a tile
+  int own_at, own_tiles, own_stride;
+  int lead;                          // first entry of its prefix unit; -1: the entry is in no group
+  int group;
+};
+struct Line {                        // the line of tiles and how blocks share it
+  int total, blocks, each, extra;    // block i has `each` steps, the first `extra` blocks one more
+  __device__ __forceinline__ Line(int all, int grid) {
+    total = all;
+    blocks = max(1, min(grid, all));
+    each = all / blocks;
+    extra = all - each * blocks;
+  }
+  __device__ __forceinline__ int start(int i) const { return i * each + min(i, extra); }
+  __device__ __forceinline__ int block_of(int x) const {
+    const int cut = extra * (each + 1);
+    return x < cut ? x / (each + 1) : extra + (x - cut) / each;
+  }
+};
 
 struct AttnParams {
   int B, n_groups, max_pages, n_pages, Hq, Hkv, G, MB;   // MB: entries of a stream's rows
+  int grid;
   float c;                           // scale x log2(e)
   const int32_t *page_table, *positions, *group_start, *prefix_lens;
-  // partial results: [slot][stream][row] of split units, [stream][b][hq] of
-  // whole ones (prefix, then own tokens)
+  // partial results: [slot][stream][row] of split units, [kind][stream][b][hq]
+  // of whole ones (prefix, then own tokens)
   float* part;
   float2* part_ml;
-  long long* tab;                    // see Table
+  Entry* entries;                    // [B], and the line's length behind them
   int n_slots;
+  const void *q, *k_pool, *v_pool;   // for rows computed alone
+  long long q_stride;
   void* out;
   float* lse;
   int32_t* status;
 };
 
-// What the joining launch needs of the line of tiles, written by block 0:
-// tab[0] its length, tab[1] the blocks that share it, then per entry the place
-// of its first prefix tile (entries that lead a unit), of its first own tile,
-// the number of both, and its unit's leader (-1: the entry is in no group).
-struct Table {
-  long long* t;
-  int B;
-  __device__ long long& total() const { return t[0]; }
-  __device__ long long& blocks() const { return t[1]; }
-  __device__ long long& prefix_at(int b) const { return t[2 + b]; }
-  __device__ long long& own_at(int b) const { return t[2 + B + b]; }
-  __device__ int& prefix_tiles(int b) const { return reinterpret_cast<int*>(t + 2 + 2 * B)[b]; }
-  __device__ int& own_tiles(int b) const { return reinterpret_cast<int*>(t + 2 + 2 * B)[B + b]; }
-  __device__ int& leader(int b) const { return reinterpret_cast<int*>(t + 2 + 2 * B)[2 * B + b]; }
-};
-__host__ __device__ inline size_t table_bytes(int B) { return 8 * (2 + 2 * (size_t)B) + 12 * (size_t)B; }
-
-// The line's block that tile x (its place in the line) falls to, and the first
-// place of block i's stretch.
-__device__ __forceinline__ int block_of(long long x, long long total, long long blocks) {
-  return (int)(((x + 1) * blocks - 1) / total);
-}
-__device__ __forceinline__ long long stretch(long long i, long long total, long long blocks) {
-  return i * total / blocks;
+// Row of `part` that holds a share of a whole unit.
+__device__ __forceinline__ size_t whole_row(const AttnParams& p, int kind, int stream, int b, int hq) {
+  return (size_t)p.n_slots * 2 * kRows + (((size_t)kind * 2 + stream) * p.B + b) * p.Hq + hq;
 }
 
-struct Segment {      // a block's share of a unit
+// A block's share of a unit.  Consecutive items whose rows share O make a run.
+struct Item {
   int head;           // KV head
-  int b0, nmem;       // entries b0 .. b0 + nmem - 1
-  int row;            // page-table row of the keys
-  int tok0;           // first token of the unit's first tile (a page start)
-  int lo, hi;         // tokens lo .. hi - 1 belong to the unit
-  int limit;          // entry b sees tokens below min(seen(b), limit)
+  int b0, nmem;       // entries b0 .. b0 + nmem - 1 hold the rows
+  int row;            // page-table row of the keys; with `own`, the one entry that meets them
+  int lo, hi;         // tokens lo .. hi - 1 belong to the unit; its first tile starts at lo's page
   int t0, t1;         // tiles
-  int dual;           // both streams share each tile
-  int slot;           // partial: split slot, or -1 prefix / -2 own for whole units
+  int j0, steps;      // steps of the run before the item, and of the whole run
+  short slot;         // partial: split slot, or -1 whole
+  bool dual;          // both streams share each tile
+  bool own;
 };
 
 template <int HD>
@@ -110,8 +125,7 @@ struct Layout {
   static constexpr int kStages = HD == 128 ? 5 : 10;
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTileBytes;
-  static constexpr int kEnd = kRing + kStages * kTileBytes;
-  static constexpr int kDyn = kEnd;
+  static constexpr int kDyn = kRing + kStages * kTileBytes;
 };
 
 // ------------------------------------------------------------------- PTX --
@@ -154,6 +168,34 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const void* map, int x, int
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// Pairs of floats in one 64-bit register: one instruction for two.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The largest of three; NaN if any is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -210,11 +252,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       MK_I4(r, 28), "r"(addr)
       : "memory");
 }
+// 16 columns
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15};" ::MK_I4(r, 0), MK_I4(r, 4), MK_I4(r, 8), MK_I4(r, 12), "r"(addr)
+      : "memory");
+}
 #undef MK_R4
 #undef MK_I4
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#define MK_W8(r, i)                                                                            \
+  "+r"((r)[i]), "+r"((r)[(i) + 1]), "+r"((r)[(i) + 2]), "+r"((r)[(i) + 3]), "+r"((r)[(i) + 4]), \
+      "+r"((r)[(i) + 5]), "+r"((r)[(i) + 6]), "+r"((r)[(i) + 7])
+// Tied to the registers of the load, so that no use of them moves up.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : MK_W8(r, 0), MK_W8(r, 8), MK_W8(r, 16), MK_W8(r, 24)::"memory");
 }
+#undef MK_W8
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -231,17 +286,16 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t lead_bytes) 
 struct Bars {
   uint64_t full[10], empty[10];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_ready[2];
-  uint64_t o_full[2], o_free[2], ml_full[2];
+  uint64_t s_full[2], p_ready[4];    // p_ready: two halves of a tile's tokens per stream
+  uint64_t o_full[2], o_free[2];
 };
 
 struct Block {
   Bars bars;
-  Segment seg[kMaxSegments];
-  float2 ml[kRows];                  // a stream's (m, l), handed to the other
-  long long scan[kWarps][4];
-  int n_seg;                         // segments of this pass
-  int total_seg;
+  Item items[kMaxItems];
+  int scan[kWarps][4];
+  int first, last;                   // units of the block's stretch
+  int win_lo, win_hi;                // stretch of this pass
   int n_steps;
   uint32_t tmem;
   int abort;
@@ -269,249 +323,313 @@ __device__ __forceinline__ bool wait(Block& s, uint32_t bar, uint32_t parity, co
 
 // ----------------------------------------------------------------- steps --
 // The block's steps, in order: one S tile each.  Step n belongs to stream
-// n & 1.  A segment with both halves of the rows has two steps per tile.  Tiles
-// are loaded in the order the MMA warp first needs them: K of steps 0 and 1,
-// then for each n V of step n and K of step n + 2.
+// n & 1.  An item with two tiles of rows has two steps per tile.  Tiles are
+// loaded in the order the MMA warp first needs them: K of steps 0 and 1, then
+// for each n V of step n and K of step n + 2.
 struct Walk {
-  const Segment* seg;
-  int n_seg;
-  int i = 0, j = 0;                  // segment, step of it
-  __device__ __forceinline__ Walk(const Segment* s, int n) : seg(s), n_seg(n) {}
-  __device__ __forceinline__ bool done() const { return i >= n_seg; }
-  __device__ __forceinline__ const Segment& at() const { return seg[i]; }
-  __device__ __forceinline__ int steps() const {
-    return (seg[i].t1 - seg[i].t0) << (seg[i].dual ? 1 : 0);
+  const Item* items;
+  int n;
+  int i = 0, j = 0, run = 0;         // item, step of it, run
+  int count = 0, j0 = 0, total = 0;  // the item's steps, those of the run before it and in all
+  bool dual = false;
+  __device__ __forceinline__ Walk(const Item* it, int n_items) : items(it), n(n_items) { enter(); }
+  __device__ __forceinline__ void enter() {
+    if (i >= n) return;
+    const Item& q = items[i];
+    dual = q.dual;
+    count = (q.t1 - q.t0) << (dual ? 1 : 0);
+    j0 = q.j0;
+    total = q.steps;
   }
-  __device__ __forceinline__ int tile() const { return seg[i].t0 + (seg[i].dual ? j >> 1 : j); }
-  __device__ __forceinline__ bool loads() const { return !(seg[i].dual && (j & 1)); }   // a new tile
-  __device__ __forceinline__ bool frees() const { return !seg[i].dual || (j & 1); }     // its last use
-  __device__ __forceinline__ bool first() const { return j == 0; }
-  __device__ __forceinline__ bool last() const { return j == steps() - 1; }
-  __device__ __forceinline__ bool first_of_stream() const { return j < 2; }
-  __device__ __forceinline__ bool last_of_stream() const { return j >= steps() - 2; }
+  __device__ __forceinline__ bool done() const { return i >= n; }
+  __device__ __forceinline__ const Item& at() const { return items[i]; }
+  __device__ __forceinline__ int tile() const { return items[i].t0 + (dual ? j >> 1 : j); }
+  __device__ __forceinline__ bool loads() const { return !(dual && (j & 1)); }   // a new tile
+  __device__ __forceinline__ bool frees() const { return !dual || (j & 1); }     // its last use
+  __device__ __forceinline__ bool enters() const { return j == 0; }
+  __device__ __forceinline__ bool first() const { return j0 + j == 0; }          // of the run
+  __device__ __forceinline__ bool last() const { return j0 + j == total - 1; }
+  __device__ __forceinline__ bool first_of_stream() const { return j0 + j < 2; }
+  __device__ __forceinline__ bool last_of_stream() const { return j0 + j >= total - 2; }
+  __device__ __forceinline__ int q_slot(int stream) const { return dual ? stream : (run & 1); }
   __device__ __forceinline__ void next() {
-    if (++j == steps()) {
+    if (last()) ++run;
+    if (++j == count) {
       j = 0;
       ++i;
+      enter();
     }
   }
 };
 
-// Where a segment's query rows lie: half s in slot s, or, when one tile of rows
-// serves both streams, slot (segment & 1).
-__device__ __forceinline__ int q_slot(const Walk& w, int stream) {
-  return w.at().dual ? stream : (w.i & 1);
-}
-
 // ------------------------------------------------------------------ list --
-// Sums of up to four numbers over lower threads; *total gets those of all.
-__device__ void scan4(Block& s, const long long* v, long long* below, long long* total) {
+// Sums of four numbers over lower threads; *total gets those of all.
+__device__ void scan4(Block& s, const int* v, int* below, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long inc[4];
+  int inc[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     inc[i] = v[i];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(kFull, inc[i], o);
+      const int up = __shfl_up_sync(kFull, inc[i], o);
       if (lane >= o) inc[i] += up;
     }
   }
-  __syncthreads();
-  if (lane == 31)
-    for (int i = 0; i < 4; ++i) s.scan[warp][i] = inc[i];
+  if (lane == 31) *reinterpret_cast<int4*>(s.scan[warp]) = make_int4(inc[0], inc[1], inc[2], inc[3]);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    long long base = 0, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) base = all;
-      all += s.scan[w][i];
+  for (int i = 0; i < 4; ++i) total[i] = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int4 t = *reinterpret_cast<const int4*>(s.scan[w]);
+    if (w == warp) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) below[i] = total[i] + inc[i] - v[i];
     }
-    below[i] = base + inc[i] - v[i];
-    total[i] = all;
+    total[0] += t.x;
+    total[1] += t.y;
+    total[2] += t.z;
+    total[3] += t.w;
   }
 }
 
-// Fills s.seg with segments [skip, skip + kMaxSegments) of this block's
-// stretch.  `tmp` is shared memory of 3 B + 2 (n_groups + 1) words, idle now.
-__device__ void list_segments(Block& s, const AttnParams& p, int32_t* tmp, int skip) {
-  int32_t* gs = tmp;                               // [n_groups + 1]
-  int32_t* pl = gs + p.n_groups + 1;               // [n_groups]
-  int32_t* seen = pl + p.n_groups + 1;             // [B]
-  int32_t* group = seen + p.B;                     // [B]; -1: none
-  int32_t* most = group + p.B;                     // [B]: prefix tokens that a leader's unit sees
+// Words of shared memory that list_items needs.
+__host__ __device__ constexpr int list_words(int batch, int groups) {
+  return 2 * (groups + 1) + 6 * batch + 2;
+}
+static_assert(list_words(kMaxBatch, kMaxBatch) * 4 <= Layout<128>::kDyn - Layout<128>::kRing &&
+                  list_words(kMaxBatch, kMaxBatch) * 4 <= Layout<64>::kDyn - Layout<64>::kRing,
+              "the list's scratch does not fit the ring");
+
+// Fills s.items with items [skip, skip + kMaxItems) of this block's stretch;
+// returns how many there are in all.  `tmp` is list_words of shared memory,
+// idle now.
+__device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip) {
+  const int n = p.n_groups, B = p.B;
+  int32_t* gs = tmp;                               // [n + 1]
+  int32_t* pl = gs + n + 1;                        // [n]
+  int32_t* seen = pl + n + 1;                      // [B]
+  int32_t* group = seen + B;                       // [B]; -1: none
+  int32_t* most = group + B;                       // [B]: prefix tokens that a leader's unit sees
+  int32_t* ppre = most + B;                        // [B]: steps of the prefix units led below
+  int32_t* pre = ppre + B;                         // [B + 1]: own tiles of lower entries
+  int32_t* cnt = pre + B + 1;                      // [B + 1]: lower entries that have any
   const int limit = p.max_pages * kPageTokens;
-  for (int i = threadIdx.x; i <= p.n_groups; i += kThreads) {
-    gs[i] = __ldg(p.group_start + i);
-    if (i < p.n_groups) pl[i] = min(max(__ldg(p.prefix_lens + i), 0), limit);
-  }
-  __syncthreads();
-  const bool teller = blockIdx.x == 0 && skip == 0;
-  if (teller) {
-    for (int i = threadIdx.x; i < p.n_groups; i += kThreads) {
-      if (gs[i] < 0 || gs[i] > gs[i + 1] || gs[i + 1] > p.B)
-        report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, i, gs[i + 1], p.B);
-      const int len = __ldg(p.prefix_lens + i);
-      if (len != pl[i]) report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, i, len, limit);
-    }
-  }
-  for (int b = threadIdx.x; b < p.B; b += kThreads) {
-    const int pos = __ldg(p.positions + b);
-    int n = pos + 1;
-    if (pos < 0) n = 0;
-    if (pos < -1 || pos >= limit) {
-      if (teller) report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, b, pos, limit);
-      n = 0;
-    }
-    int g = -1;
-    if (p.n_groups > 0) {
-      int lo = 0, hi = p.n_groups;                 // last group that starts at or before b
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (gs[mid] <= b) lo = mid;
-        else hi = mid;
+  const bool teller = blockIdx.x == gridDim.x - 1 && skip == 0;
+  bool bad = false;                  // group bounds out of order: nothing is in a group
+  for (int i = threadIdx.x; i <= n; i += kThreads) {
+    const int from = __ldg(p.group_start + i);
+    gs[i] = from;
+    if (i < n) {
+      const int to = __ldg(p.group_start + i + 1);
+      if (from < 0 || from > to || to > B) {
+        bad = true;
+        if (teller) report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, i, to, B);
       }
-      if (gs[lo] >= 0 && gs[lo] <= b && b < gs[lo + 1]) g = lo;
+      const int len = __ldg(p.prefix_lens + i), fit = min(max(len, 0), limit);
+      pl[i] = fit;
+      if (teller && len != fit) report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, i, len, limit);
     }
-    seen[b] = n;
-    group[b] = g;
+  }
+  for (int b = threadIdx.x; b < B; b += kThreads) {
+    const int pos = __ldg(p.positions + b);
+    const bool fits = pos >= -1 && pos < limit;
+    if (teller && !fits) report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, b, pos, limit);
+    seen[b] = fits ? pos + 1 : 0;
     most[b] = 0;
   }
-  __syncthreads();
+  if (threadIdx.x == 0) {
+    s.first = INT32_MAX;
+    s.last = -1;
+    s.n_steps = 0;
+  }
+  bad = __syncthreads_or(bad);
   const int span = 2 * p.MB;                       // entries of a prefix unit
-  for (int b = threadIdx.x; b < p.B; b += kThreads) {
-    const int g = group[b];
-    if (g >= 0) {
-      const int lead = b - (b - gs[g]) % span;
-      if (group[lead] == g) atomicMax(&most[lead], min(seen[b], pl[g]));
+  auto lead_of = [&](int b, int g) { return b - (b - gs[g]) % span; };
+  for (int b = threadIdx.x; b < B; b += kThreads) {
+    int lo = 0, hi = n;                            // last group that starts at or before b
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (gs[mid] <= b) lo = mid;
+      else hi = mid;
     }
+    const int g = !bad && gs[lo] <= b && b < gs[lo + 1] ? lo : -1;
+    group[b] = g;
+    if (g >= 0) atomicMax(&most[lead_of(b, g)], min(seen[b], pl[g]));
   }
   __syncthreads();
   // this thread's entries: places of their tiles in the line
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int e0 = min(p.B, (int)threadIdx.x * per), e1 = min(p.B, e0 + per);
+  const int per = (B + kThreads - 1) / kThreads;
+  const int e0 = min(B, (int)threadIdx.x * per), e1 = min(B, e0 + per);
+  auto members = [&](int b) { return min(min(span, gs[group[b] + 1] - b), B - b); };
+  auto width = [&](int b) { return members(b) > p.MB ? 2 : 1; };
   auto prefix_tiles = [&](int b) { return (most[b] + kTile - 1) / kTile; };
-  auto own_first = [&](int b) { return pl[group[b]] / kPageTokens * kPageTokens; };
   auto own_tiles = [&](int b) {
     const int g = group[b];
     if (g < 0 || seen[b] <= pl[g]) return 0;
-    return (seen[b] - own_first(b) + kTile - 1) / kTile;
+    return (seen[b] - pl[g] / kPageTokens * kPageTokens + kTile - 1) / kTile;
   };
-  long long v[4] = {0, 0, 0, 0}, below[4], total[4];
+  int v[4] = {0, 0, 0, 0}, below[4], total[4];     // prefix steps, prefix units, own tiles, own units
   for (int b = e0; b < e1; ++b) {
-    v[0] += (long long)prefix_tiles(b) * p.Hkv;
-    v[1] += (long long)own_tiles(b) * p.Hkv;
+    const int np = prefix_tiles(b), no = own_tiles(b);
+    if (np) {
+      v[0] += np * width(b);
+      v[1] += 1;
+    }
+    v[2] += no;
+    v[3] += no > 0;
   }
   scan4(s, v, below, total);
-  const long long all = total[0] + total[1];
-  const long long blocks = max(1ll, min((long long)gridDim.x, all));
-  if (teller) {
-    const Table tab{p.tab, p.B};
-    if (threadIdx.x == 0) {
-      tab.total() = all;
-      tab.blocks() = blocks;
-    }
-    long long pa = below[0], oa = total[0] + below[1];
+  {
+    int steps = below[0], tiles = below[2], units = below[3];
     for (int b = e0; b < e1; ++b) {
-      const int g = group[b];
+      ppre[b] = steps;
+      pre[b] = tiles;
+      cnt[b] = units;
       const int np = prefix_tiles(b), no = own_tiles(b);
-      tab.prefix_at(b) = pa;
-      tab.own_at(b) = oa;
-      tab.prefix_tiles(b) = np;
-      tab.own_tiles(b) = no;
-      tab.leader(b) = g < 0 ? -1 : b - (b - gs[g]) % span;
-      pa += (long long)np * p.Hkv;
-      oa += (long long)no * p.Hkv;
+      if (np) steps += np * width(b);
+      tiles += no;
+      units += no > 0;
+    }
+    if (threadIdx.x == 0) {
+      pre[B] = total[2];
+      cnt[B] = total[3];
     }
   }
-  long long r0 = 0, r1 = 0;
-  if (all > 0 && (long long)blockIdx.x < blocks) {
-    r0 = stretch(blockIdx.x, all, blocks);
-    r1 = stretch(blockIdx.x + 1, all, blocks);
+  __syncthreads();
+  const int own0 = p.Hkv * total[0];               // place of the first own tile
+  const Line line(own0 + p.Hkv * total[2], p.grid);
+  auto chunk_of = [&](int b) { return b / p.MB * p.MB; };
+  if (teller) {
+    if (threadIdx.x == 0) reinterpret_cast<int*>(p.entries + B)[0] = line.total;
+    for (int b = threadIdx.x; b < B; b += kThreads) {
+      const int g = group[b], cf = chunk_of(b), ce = min(B, cf + p.MB);
+      Entry e{};
+      e.lead = -1;
+      if (g >= 0) {
+        e.lead = lead_of(b, g);
+        e.group = g;
+        e.prefix_tiles = prefix_tiles(e.lead);
+        if (e.prefix_tiles) {
+          e.prefix_width = width(e.lead);
+          e.prefix_at = p.Hkv * ppre[e.lead];
+        }
+        e.own_tiles = own_tiles(b);
+        e.own_stride = pre[ce] - pre[cf];
+        e.own_at = own0 + (p.Hkv - 1) * pre[cf] + pre[b];
+      }
+      p.entries[b] = e;
+    }
   }
-  // count this thread's segments, then write them at their places
+  int r0 = 0, r1 = 0;
+  if (line.total > 0 && (int)blockIdx.x < line.blocks) {
+    r0 = line.start(blockIdx.x);
+    r1 = line.start(blockIdx.x + 1);
+  }
+  // this thread's units that fall to the stretch: (prefix, entry, head, place
+  // in the line, tiles of the unit, share t0 .. t1 - 1, number of the unit)
   auto visit = [&](auto&& emit) {
-    long long at = below[0];
+    int units = p.Hkv * below[1];
     for (int b = e0; b < e1; ++b) {
       const int nt = prefix_tiles(b);
-      const long long end = at + (long long)nt * p.Hkv;
-      if (nt > 0 && end > r0 && at < r1) {
-        for (int h = (int)max(0ll, (r0 - at) / nt); h < p.Hkv; ++h) {
-          const long long us = at + (long long)h * nt;
+      if (nt == 0) continue;
+      const int w = width(b), at = p.Hkv * ppre[b];
+      if (at < r1 && at + p.Hkv * nt * w > r0) {
+        for (int h = max(0, (r0 - at) / (nt * w)); h < p.Hkv; ++h) {
+          const int us = at + h * nt * w;
           if (us >= r1) break;
-          const int t0 = (int)max(0ll, r0 - us), t1 = (int)min((long long)nt, r1 - us);
-          if (t1 > t0) emit(true, b, h, nt, t0, t1);
+          const int t0 = max(0, (r0 - us + w - 1) >> (w - 1)), t1 = min(nt, (r1 - us + w - 1) >> (w - 1));
+          if (t1 > t0) emit(true, b, h, us, nt, t0, t1, units + h);
         }
       }
-      at = end;
+      units += p.Hkv;
     }
-    at = total[0] + below[1];
+    units = p.Hkv * total[1];
     for (int b = e0; b < e1; ++b) {
       const int nt = own_tiles(b);
-      const long long end = at + (long long)nt * p.Hkv;
-      if (nt > 0 && end > r0 && at < r1) {
-        for (int h = (int)max(0ll, (r0 - at) / nt); h < p.Hkv; ++h) {
-          const long long us = at + (long long)h * nt;
-          if (us >= r1) break;
-          const int t0 = (int)max(0ll, r0 - us), t1 = (int)min((long long)nt, r1 - us);
-          if (t1 > t0) emit(false, b, h, nt, t0, t1);
-        }
+      if (nt == 0) continue;
+      const int cf = chunk_of(b), ce = min(B, cf + p.MB), stride = pre[ce] - pre[cf];
+      const int at = own0 + (p.Hkv - 1) * pre[cf] + pre[b];
+      if (at >= r1 || at + (p.Hkv - 1) * stride + nt <= r0) continue;
+      for (int h = max(0, (r0 - at - nt) / stride); h < p.Hkv; ++h) {
+        const int us = at + h * stride;
+        if (us >= r1) break;
+        const int t0 = max(0, r0 - us), t1 = min(nt, r1 - us);
+        if (t1 > t0)
+          emit(false, b, h, us, nt, t0, t1,
+               units + (p.Hkv - 1) * cnt[cf] + h * (cnt[ce] - cnt[cf]) + cnt[b]);
       }
-      at = end;
     }
   };
-  long long n[4] = {0, 0, 0, 0}, nb[4], nt_all[4];
-  visit([&](bool prefix, int, int, int, int, int) { n[prefix ? 0 : 1] += 1; });
-  scan4(s, n, nb, nt_all);
-  long long place[2] = {nb[0], nt_all[0] + nb[1]};
-  const int total_seg = (int)(nt_all[0] + nt_all[1]);
-  if (threadIdx.x == 0) {
-    s.total_seg = total_seg;
-    s.n_seg = min(kMaxSegments, total_seg - skip);
-  }
-  visit([&](bool prefix, int b, int h, int nt, int t0, int t1) {
-    const long long at = place[prefix ? 0 : 1]++ - skip;
-    if (at < 0 || at >= kMaxSegments) return;
-    const int g = group[b];
-    Segment& q = s.seg[at];
-    q.head = h;
-    q.b0 = b;
-    q.t0 = t0;
-    q.t1 = t1;
-    if (prefix) {
-      q.nmem = min(min(span, gs[g + 1] - b), p.B - b);
-      q.row = gs[g];
-      q.tok0 = 0;
-      q.lo = 0;
-      q.hi = most[b];
-      q.limit = pl[g];
-    } else {
-      q.nmem = 1;
-      q.row = b;
-      q.tok0 = own_first(b);
-      q.lo = pl[g];
-      q.hi = seen[b];
-      q.limit = seen[b];
-    }
-    q.dual = q.nmem > p.MB;
-    const bool whole = t0 == 0 && t1 == nt;
-    q.slot = whole ? (prefix ? -1 : -2) : 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
+  visit([&](bool, int, int, int, int, int, int, int unit) {
+    atomicMin(&s.first, unit);
+    atomicMax(&s.last, unit);
   });
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int steps = 0;
-    for (int i = 0; i < s.n_seg; ++i) steps += (s.seg[i].t1 - s.seg[i].t0) << (s.seg[i].dual ? 1 : 0);
-    s.n_steps = steps;
+  const int first = s.first + skip;
+  const int n_items = s.last < 0 ? 0 : s.last - s.first + 1;
+  if (n_items > kMaxItems) {         // more than one pass: the runs end with a pass
+    if (threadIdx.x == 0) {
+      s.win_lo = r0;
+      s.win_hi = r1;
+    }
+    __syncthreads();
+    visit([&](bool, int, int, int us, int, int t0, int, int unit) {
+      if (unit == first) s.win_lo = us + t0;
+      if (unit == first + kMaxItems) s.win_hi = us;
+    });
+    __syncthreads();
+    r0 = max(r0, s.win_lo);
+    r1 = min(r1, s.win_hi);
   }
+  visit([&](bool prefix, int b, int h, int us, int nt, int t0, int t1, int unit) {
+    if (unit < first || unit >= first + kMaxItems) return;
+    const int g = group[b];
+    Item& q = s.items[unit - first];
+    q.head = h;
+    q.t0 = t0;
+    q.t1 = t1;
+    q.own = !prefix;
+    if (prefix) {
+      q.b0 = b;
+      q.nmem = members(b);
+      q.row = gs[g];
+      q.lo = 0;
+      q.hi = most[b];
+      q.dual = q.nmem > p.MB;
+      q.j0 = 0;
+      q.steps = (t1 - t0) << (q.dual ? 1 : 0);
+      atomicAdd(&s.n_steps, q.steps);
+    } else {
+      q.b0 = chunk_of(b);
+      q.nmem = min(p.MB, B - q.b0);
+      q.row = b;
+      q.lo = pl[g];
+      q.hi = seen[b];
+      q.dual = false;
+      // the run: the chunk's own tiles of this head, as far as they are here
+      const int stride = pre[q.b0 + q.nmem] - pre[q.b0];
+      const int hs = us - (pre[b] - pre[q.b0]);
+      const int from = max(r0, hs), to = min(r1, hs + stride);
+      q.j0 = us + t0 - from;
+      q.steps = to - from;
+      atomicAdd(&s.n_steps, t1 - t0);
+    }
+    const bool whole = t0 == 0 && t1 == nt;
+    q.slot = (short)(whole ? -1 : 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0));
+  });
   __syncthreads();
+  return n_items;
 }
 
-// Whether a tile has tokens inside its loaded pages that nobody may see: what
-// lies there is not the sequence's, and 0 x infinity would spoil the row.
-__device__ __forceinline__ bool ragged(const Segment& q, int tile) {
-  const int a = q.tok0 + tile * kTile;
-  return a < q.lo || a + kTile > q.hi;
+// Whether a tile has tokens inside its loaded pages that are not the unit's:
+// what lies there is not the sequence's, and 0 x infinity would spoil the row.
+__device__ __forceinline__ bool ragged(const Item& q, int at) {
+  return at < q.lo || (at + kTile > q.hi && (q.hi & (kPageTokens - 1)) != 0);
+}
+__device__ __forceinline__ int first_token(const Item& q, int tile) {
+  return q.lo / kPageTokens * kPageTokens + tile * kTile;
 }
 
 template <typename T>
@@ -538,6 +656,32 @@ struct Half<__half> {
   }
 };
 
+// 2^y for a pair on the FMA pipe: y = n + f with |f| <= 1/2, a polynomial of
+// degree 4 in f (least-squares fit of the relative error, 2.8e-6 at most) and n
+// added to the exponent.  Below -127 it is 0; a NaN need not stay one.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t y) {
+  float a, b;
+  unpair(y, a, b);
+  y = pair(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
+  constexpr float kMagic = 12582912.0f;                  // 1.5 x 2^23: rounds to an integer
+  const uint64_t t = add2(y, pair(kMagic, kMagic));
+  const uint64_t n = add2(t, pair(-kMagic, -kMagic));
+  const uint64_t f = fma2(n, pair(-1.0f, -1.0f), y);
+  uint64_t r = fma2(f, pair(0.00958285f, 0.00958285f), pair(0.05590643f, 0.05590643f));
+  r = fma2(r, f, pair(0.24024099f, 0.24024099f));
+  r = fma2(r, f, pair(0.6931242f, 0.6931242f));
+  r = fma2(r, f, pair(1.0f, 1.0f));
+  float ta, tb, ra, rb;
+  unpair(t, ta, tb);
+  unpair(r, ra, rb);
+  return pair(__uint_as_float(__float_as_uint(ra) + (__float_as_uint(ta) << 23)),
+              __uint_as_float(__float_as_uint(rb) + (__float_as_uint(tb) << 23)));
+}
+
+// Pairs of every 16 whose exponentials the FMA pipe takes over from the
+// special-function unit, which alone would bound the softmax.
+constexpr int kFmaPairs = 6;
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
@@ -547,16 +691,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t base[];
   __shared__ Block s;
   const uint32_t sb = saddr(base);
-  if (sb & 1023) {                   // the swizzled tiles would not line up
-    report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, -1, (int)sb, 1024);
-    return;
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t b_full = saddr(s.bars.full), b_empty = saddr(s.bars.empty);
   const uint32_t b_qfull = saddr(s.bars.q_full), b_qempty = saddr(s.bars.q_empty);
   const uint32_t b_sfull = saddr(s.bars.s_full), b_pready = saddr(s.bars.p_ready);
   const uint32_t b_ofull = saddr(s.bars.o_full), b_ofree = saddr(s.bars.o_free);
-  const uint32_t b_ml = saddr(s.bars.ml_full);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
@@ -567,13 +706,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(b_qfull + 8 * i, 1);
       mbar_init(b_qempty + 8 * i, 1);
       mbar_init(b_sfull + 8 * i, 1);
-      mbar_init(b_pready + 8 * i, kGroupThreads);
+      mbar_init(b_pready + 16 * i, kGroupThreads);
+      mbar_init(b_pready + 16 * i + 8, kGroupThreads);
       mbar_init(b_ofull + 8 * i, 1);
       mbar_init(b_ofree + 8 * i, kGroupThreads);
-      mbar_init(b_ml + 8 * i, kGroupThreads);
     }
     s.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+    prefetch_map(&qmap);
+    prefetch_map(&qmap_one);
   }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -581,77 +726,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  tc_before();
-  __syncthreads();
-  tc_after();
-  const uint32_t tm = s.tmem;
-  const uint32_t tm_s[2] = {tm, tm + 128}, tm_o[2] = {tm + 256, tm + 384};
+  // Nothing of the call's memory is touched before the kernels ahead are done.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Barrier use counts, carried from pass to pass by every role that needs them.
   uint32_t ring = 0;                 // tiles loaded so far
   uint32_t qn[2] = {0, 0};           // uses of each query slot
   uint32_t sn[2] = {0, 0};           // steps of each stream
-  uint32_t on[2] = {0, 0};           // segments of each stream
-  uint32_t mln[2] = {0, 0};          // hand-overs of each stream
+  uint32_t on[2] = {0, 0};           // runs of each stream
   bool ok = true;
+  uint32_t tm = 0;
 
-  for (int skip = 0;; skip += kMaxSegments) {
-    list_segments(s, p, reinterpret_cast<int32_t*>(base + L::kRing), skip);
-    const int n_seg = s.n_seg, n_steps = s.n_steps;
+  for (int skip = 0;; skip += kMaxItems) {
+    const int n_all = list_items(s, p, reinterpret_cast<int32_t*>(base + L::kRing), skip);
+    const int n_items = min(kMaxItems, n_all - skip), n_steps = s.n_steps;
     // the list's scratch is the ring: later writes there go through TMA
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_before();
     __syncthreads();
+    tc_after();
+    tm = s.tmem;
+    const uint32_t tm_s[2] = {tm, tm + 128}, tm_o[2] = {tm + 256, tm + 384};
 
     if (warp == kTmaWarp) {
       // -------------------------------------------------------- loads -----
-      // lane i of `kp` holds the physical page of the segment's page i + base
-      struct Pages {
-        int seg = -1, first = 0, id = 0;
-      } kc, vc;
-      auto page = [&](Pages& c, const Walk& w, int index) {
-        const Segment& q = w.at();
-        if (c.seg != w.i || index < c.first || index >= c.first + 32) {
-          c.seg = w.i;
-          c.first = index;
-          const int lp = index + lane;
-          int id = p.n_pages;                     // beyond the pool: loads as zeros
-          if (lp < p.max_pages && lp * kPageTokens < q.hi) {
-            id = __ldg(p.page_table + (size_t)q.row * p.max_pages + lp);
-            if (id < 0 || id >= p.n_pages) {
-              report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, q.row, id, p.n_pages);
-              id = p.n_pages;
-            }
-          }
-          c.id = id;
+      // Lane i holds where the two pages of tile from + i begin in the pools'
+      // rows, of 32 tiles at a time and of the 32 before.
+      int from = -32, y0 = 0, y1 = 0, y0_was = 0, y1_was = 0;
+      auto look_up = [&]() {
+        from += 32;
+        y0_was = y0;
+        y1_was = y1;
+        int x = from + lane, i = 0;
+        for (; i < n_items; ++i) {
+          const int nt = s.items[i].t1 - s.items[i].t0;
+          if (x < nt) break;
+          x -= nt;
         }
-        return __shfl_sync(kFull, c.id, index - c.first);
+        int id[2] = {p.n_pages, p.n_pages}, head = 0;    // beyond the pool: loads as zeros
+        if (i < n_items) {
+          const Item& q = s.items[i];
+          head = q.head;
+          const int page = first_token(q, q.t0 + x) / kPageTokens;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int lp = page + k;
+            if (lp < p.max_pages && lp * kPageTokens < q.hi)
+              id[k] = __ldg(p.page_table + (size_t)q.row * p.max_pages + lp);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (id[k] < 0 || id[k] > p.n_pages ||
+                (id[k] == p.n_pages && page + k < p.max_pages && (page + k) * kPageTokens < q.hi)) {
+              report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, q.row, id[k], p.n_pages);
+              id[k] = p.n_pages;
+            }
+        }
+        y0 = (id[0] * p.Hkv + head) * kPageTokens;
+        y1 = (id[1] * p.Hkv + head) * kPageTokens;
       };
-      auto load_tile = [&](Pages& c, const Walk& w, const void* map) {
-        const Segment& q = w.at();
-        const int first = (q.tok0 + w.tile() * kTile) / kPageTokens;
-        const int id0 = page(c, w, first), id1 = page(c, w, first + 1);
+      auto load_tile = [&](int tile, const void* map) {
+        if (tile >= from + 32) look_up();
+        const bool now = tile >= from;
+        const int src = now ? tile - from : tile - from + 32;
+        const int a = __shfl_sync(kFull, now ? y0 : y0_was, src);
+        const int b = __shfl_sync(kFull, now ? y1 : y1_was, src);
         const uint32_t st = ring % L::kStages, bar = b_full + 8 * st;
         if (ring >= L::kStages) ok = ok && wait(s, b_empty + 8 * st, (ring / L::kStages - 1) & 1, p);
         ok = __all_sync(kFull, ok);
         if (ok && lane == 0) {
           mbar_expect(bar, L::kTileBytes);
           const uint32_t dst = sb + L::kRing + st * L::kTileBytes;
-          const int y0 = (id0 * p.Hkv + q.head) * kPageTokens;
-          const int y1 = (id1 * p.Hkv + q.head) * kPageTokens;
 #pragma unroll
           for (int c2 = 0; c2 < L::kChunks; ++c2) {
-            tma_3d(dst + c2 * kTile * 128, map, 0, y0, c2, bar);
-            tma_3d(dst + c2 * kTile * 128 + kPageTokens * 128, map, 0, y1, c2, bar);
+            tma_3d(dst + c2 * kTile * 128, map, 0, a, c2, bar);
+            tma_3d(dst + c2 * kTile * 128 + kPageTokens * 128, map, 0, b, c2, bar);
           }
         }
         __syncwarp();
         ++ring;
       };
       auto load_q = [&](const Walk& w) {
-        const Segment& q = w.at();
+        const Item& q = w.at();
         for (int h = 0; h < (q.dual ? 2 : 1); ++h) {
-          const int sl = q_slot(w, h);
+          const int sl = w.q_slot(h);
           if (qn[sl] > 0) ok = ok && wait(s, b_qempty + 8 * sl, (qn[sl] - 1) & 1, p);
           ok = __all_sync(kFull, ok);
           if (ok && lane == 0) {
@@ -668,15 +827,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           qn[sl] += 1;
         }
       };
-      Walk k(s.seg, n_seg), v(s.seg, n_seg);
+      Walk k(s.items, n_items), v(s.items, n_items);
+      int kt = 0, vt = 0;
       auto do_k = [&]() {
         if (k.first()) load_q(k);
-        if (k.loads()) load_tile(kc, k, &kmap);
+        if (k.loads()) load_tile(kt++, &kmap);
         k.next();
       };
       for (int i = 0; i < 2 && i < n_steps && ok; ++i) do_k();
       for (int n = 0; n < n_steps && ok; ++n) {
-        if (v.loads()) load_tile(vc, v, &vmap);
+        if (v.loads()) load_tile(vt++, &vmap);
         v.next();
         if (ok && n + 2 < n_steps) do_k();
       }
@@ -687,21 +847,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                              ((uint32_t)(kRows >> 4) << 24);
         const uint32_t id_qk = fmt | ((uint32_t)(kTile >> 3) << 17);
         const uint32_t id_pv = fmt | (1u << 16) | ((uint32_t)(HD >> 3) << 17);
-        Walk k(s.seg, n_seg), v(s.seg, n_seg);
+        Walk k(s.items, n_items), v(s.items, n_items);
         uint32_t k_st = 0, v_st = 0;
         int kstep = 0;
         auto do_k = [&]() {
           const int st = kstep & 1;
-          const int sl = q_slot(k, st);
+          const int sl = k.q_slot(st);
           if (k.loads()) {
             k_st = ring % L::kStages;
             ok = ok && wait(s, b_full + 8 * k_st, (ring / L::kStages) & 1, p);
             ++ring;
           }
           if (k.first()) {
-            const int n = k.at().dual ? 2 : 1;
+            const int n = k.dual ? 2 : 1;
             for (int h = 0; h < n; ++h) {
-              const int s2 = q_slot(k, h);
+              const int s2 = k.q_slot(h);
               ok = ok && wait(s, b_qfull + 8 * s2, qn[s2] & 1, p);
               qn[s2] += 1;
             }
@@ -717,8 +877,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_commit(b_sfull + 8 * st);
           if (k.frees()) tc_commit(b_empty + 8 * k_st);
-          // the segment's last use of a slot
-          if (k.at().dual ? k.last_of_stream() : k.last()) tc_commit(b_qempty + 8 * sl);
+          // the run's last use of a slot
+          if (k.dual ? k.last_of_stream() : k.last()) tc_commit(b_qempty + 8 * sl);
           k.next();
           ++kstep;
         };
@@ -731,15 +891,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++ring;
           }
           if (v.first_of_stream() && on[st] > 0) ok = ok && wait(s, b_ofree + 8 * st, (on[st] - 1) & 1, p);
-          ok = ok && wait(s, b_pready + 8 * st, sn[st] & 1, p);
+          const uint32_t va = sb + L::kRing + v_st * L::kTileBytes;
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && wait(s, b_pready + 16 * st + 8 * half, sn[st] & 1, p);
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int k4 = 0; k4 < kTile / 32; ++k4) {
+              const int kk = half * (kTile / 32) + k4;
+              mma_ts(tm_o[st], tm_s[st] + kk * 8, desc_of(va + kk * 16 * 128, kTile * 128), id_pv,
+                     !(v.first_of_stream() && kk == 0));
+            }
+          }
           if (!ok) break;
           sn[st] += 1;
-          tc_after();
-          const uint32_t va = sb + L::kRing + v_st * L::kTileBytes;
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ts(tm_o[st], tm_s[st] + kk * 8, desc_of(va + kk * 16 * 128, kTile * 128), id_pv,
-                   !(v.first_of_stream() && kk == 0));
           if (v.frees()) tc_commit(b_empty + 8 * v_st);
           if (v.last_of_stream()) {
             tc_commit(b_ofull + 8 * st);
@@ -756,41 +921,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = threadIdx.x & (kGroupThreads - 1); // row
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 lanes
       const uint32_t ts = tm_s[st] + lanes;
-      Walk w(s.seg, n_seg);
+      Walk w(s.items, n_items);
       uint32_t kloads = 0, vloads = 0;                 // among the steps so far
       float m = -INFINITY, l = 0.0f;
-      bool real = false, busy = false;
-      int lim = 0;
+      const int j = r / p.G;                           // entry among the rows, less b0
+      bool busy = false, shared = false;               // rows of this warp meet the item; have to be 0
+      int slot = -2, lim = 0;                          // the row's partial result; -2: none
       for (int n = 0; n < n_steps && ok; ++n) {
-        const Segment& q = w.at();
+        const Item& q = w.at();
         if (w.loads()) {
           ++kloads;
           ++vloads;
         }
         if (w.first()) {
-          // this thread's row of the segment
-          const int j = r / p.G, e = (q.dual ? st * p.MB : 0) + j;
-          real = j < p.MB && e < q.nmem;
-          busy = __any_sync(kFull, real);
-          lim = INT32_MAX;
-          if (real) {
-            const int pos = __ldg(p.positions + q.b0 + e);
-            lim = min(pos < 0 || pos >= p.max_pages * kPageTokens ? 0 : pos + 1, q.limit);
-          }
+          m = -INFINITY;
+          l = 0.0f;
+          slot = -2;
         }
-        if ((n & 1) != st) {
-          if (!w.last()) {
-            w.next();
-            continue;
+        if (w.enters()) {
+          // this thread's row of the item
+          const int e = (w.dual ? st * p.MB : 0) + j;
+          const bool real = j < p.MB && (q.own ? q.b0 + e == q.row : e < q.nmem);
+          shared = q.own;
+          busy = __any_sync(kFull, real);
+          lim = 0;
+          if (real) {
+            slot = q.slot;
+            lim = q.hi;
+            if (!q.own) {
+              const int pos = __ldg(p.positions + q.b0 + e);
+              lim = min(pos < 0 || pos >= p.max_pages * kPageTokens ? 0 : pos + 1, q.hi);
+            }
           }
         }
         if ((n & 1) == st) {
-          if (w.first_of_stream()) {
-            m = -INFINITY;
-            l = 0.0f;
+          const int a = first_token(q, w.tile());
+          ok = ok && wait(s, b_sfull + 8 * st, sn[st] & 1, p);
+          if (!__all_sync(kFull, ok)) {
+            ok = false;
+            break;
           }
-          const int a = q.tok0 + w.tile() * kTile;
-          if (ragged(q, w.tile())) {
+          sn[st] += 1;
+          uint32_t x[32], y[32];
+          float f_old = 1.0f, ref = 0.0f;
+          const bool masked = __any_sync(kFull, a < q.lo || a + kTile > lim);
+          // scores of tokens that are not the row's, in columns c .. c + 31
+          auto mask = [&](uint32_t* v, int c) {
+            if (!masked) return;
+            const int lo = q.lo - a - c, hi = lim - a - c;
+            const uint32_t below = lo <= 0 ? 0u : lo >= 32 ? kFull : (1u << lo) - 1u;
+            const uint32_t keep = (hi <= 0 ? 0u : hi >= 32 ? kFull : (1u << hi) - 1u) & ~below;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((keep >> i) & 1u)) v[i] = 0xff800000u;
+          };
+          if (busy) {
+            tc_after();
+            float t0 = -INFINITY, t1 = -INFINITY;
+            auto largest = [&](const uint32_t* v) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                t0 = max3(t0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                t1 = max3(t1, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+              }
+            };
+            tmem_ld32(ts, x);
+            tmem_wait_ld32(x);
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 64) {
+              tmem_ld32(ts + c + 32, y);
+              mask(x, c);
+              largest(x);
+              tmem_wait_ld32(y);
+              tmem_ld32(ts + ((c + 64) & (kTile - 1)), x);   // at the end: the first columns again
+              mask(y, c + 32);
+              largest(y);
+              tmem_wait_ld32(x);
+            }
+            const float top = max3(t0, t1, t1) * p.c;
+            // a score that is no number, or +infinity, makes the sum NaN
+            if (top != -INFINITY) l += top - top;
+            const bool grow = top > m + kRescale;      // also the first score of a row
+            const float m_old = m;
+            if (grow) {
+              f_old = ex2(m - top);                    // 0 for the first
+              l *= f_old;
+              m = top;
+            }
+            // O of a row without a score so far is 0 already
+            if (__any_sync(kFull, grow && m_old != -INFINITY)) {
+              // S of this step was committed after P V of the stream's last
+              // one, so O is at rest
+              const uint32_t to = tm_o[st] + lanes;
+#pragma unroll 1
+              for (int i = 0; i < HD; i += 32) {
+                tmem_ld32(to + i, y);
+                tmem_wait_ld32(y);
+#pragma unroll
+                for (int k2 = 0; k2 < 32; ++k2) y[k2] = __float_as_uint(__uint_as_float(y[k2]) * f_old);
+                tmem_st32(to + i, y);
+              }
+            }
+            ref = (m == -INFINITY ? 0.0f : m) - Half<T>::kShift;
+          }
+          if (ragged(q, a)) {
             // clear V's rows of tokens that are not the unit's.  The tile's
             // place in the ring: behind the V tiles so far and the K tiles of
             // the steps up to the one after that which loaded it.
@@ -802,159 +1036,123 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(s, b_full + 8 * vs, (at / L::kStages) & 1, p);
             if (ok) {
               const uint32_t va = sb + L::kRing + vs * L::kTileBytes;
-              for (int i = r; i < kTile * L::kChunks * 8; i += kGroupThreads) {
-                const int tok = a + ((i >> 3) & (kTile - 1));
-                if (tok < q.lo || tok >= q.hi)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(va + i * 16), "r"(0)
-                               : "memory");
+              auto clear = [&](int tok0, int tok1) {
+                for (int i = tok0 * 8 + r; i < tok1 * 8; i += kGroupThreads)
+#pragma unroll
+                  for (int c2 = 0; c2 < L::kChunks; ++c2)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                     va + c2 * kTile * 128 + i * 16),
+                                 "r"(0)
+                                 : "memory");
+              };
+              clear(0, min(max(q.lo - a, 0), kTile));
+              if (a + kTile > q.hi) {
+                const int end = max(q.hi - a, 0);
+                clear(end, min(kTile, (end + kPageTokens - 1) / kPageTokens * kPageTokens));
               }
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
+            if (!__all_sync(kFull, ok)) {
+              ok = false;
+              break;
+            }
           }
-          ok = ok && wait(s, b_sfull + 8 * st, sn[st] & 1, p);
-          if (!__all_sync(kFull, ok)) {
-            ok = false;
-            break;
-          }
-          sn[st] += 1;
           if (busy) {
-            tc_after();
-            uint32_t x[kTile];
+            const uint64_t c2 = pair(p.c, p.c), r2 = pair(-ref, -ref);
+            uint64_t sum[2] = {0, 0};
+            auto weigh = [&](const uint32_t* v, int c) {
+              uint32_t o[16];
 #pragma unroll
-            for (int i = 0; i < kTile; i += 32) tmem_ld32(ts + i, x + i);
-            tmem_wait_ld();
-            float* f = reinterpret_cast<float*>(x);
-            if (__any_sync(kFull, a < q.lo || a + kTile > lim)) {
-              const int from = q.lo - a, to = lim - a;
-#pragma unroll
-              for (int i = 0; i < kTile; ++i)
-                if (i < from || i >= to) f[i] = -INFINITY;
-            }
-            float mx[4] = {f[0], f[1], f[2], f[3]};
-#pragma unroll
-            for (int i = 4; i < kTile; ++i) mx[i & 3] = fmaxf(mx[i & 3], f[i]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
-            const bool grow = top > m + kRescale;      // also the first score of a row
-            if (__any_sync(kFull, grow)) {
-              const float m_new = grow ? top : m;
-              const float f_old = m == m_new ? 1.0f : ex2(m - m_new);
-              l *= f_old;
-              m = m_new;
-              if (!w.first_of_stream()) {
-                // S of this step was committed after P V of the stream's last
-                // one, so O is at rest
-                const uint32_t to = tm_o[st] + lanes;
-#pragma unroll 1
-                for (int i = 0; i < HD; i += 32) {
-                  uint32_t o[32];
-                  tmem_ld32(to + i, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int k2 = 0; k2 < 32; ++k2)
-                    o[k2] = __float_as_uint(__uint_as_float(o[k2]) * f_old);
-                  tmem_st32(to + i, o);
+              for (int i = 0; i < 16; ++i) {
+                uint64_t e = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), c2, r2);
+                float ea, eb;
+                if (i * kFmaPairs / 16 != (i + 1) * kFmaPairs / 16) {
+                  e = exp2_pair(e);
+                  unpair(e, ea, eb);
+                } else {
+                  unpair(e, ea, eb);
+                  ea = ex2(ea);
+                  eb = ex2(eb);
+                  e = pair(ea, eb);
                 }
+                sum[i & 1] = add2(sum[i & 1], e);
+                o[i] = Half<T>::pack(ea, eb);
               }
+              tmem_st16(ts + c / 2, o);        // over columns whose scores have been read
+            };
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 64) {
+              tmem_ld32(ts + c + 32, y);
+              mask(x, c);
+              tmem_wait_ld32(y);
+              weigh(x, c);
+              if (c == 0) tmem_ld32(ts + 64, x);
+              mask(y, c + 32);
+              weigh(y, c + 32);
+              if (c == 0) tmem_wait_ld32(x);
+              tmem_wait_st();
+              tc_before();
+              mbar_arrive(b_pready + 16 * st + (c ? 8 : 0));
             }
-            const float ref = (m == -INFINITY ? 0.0f : m) - Half<T>::kShift;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float s0, s1, s2, s3;
+            unpair(sum[0], s0, s1);
+            unpair(sum[1], s2, s3);
+            l += (s0 + s1) + (s2 + s3);
+          } else {
+            if (shared) {              // other entries' tokens: no weight
+              tc_after();
 #pragma unroll
-            for (int i = 0; i < kTile; i += 2) {
-              const float pa = ex2(fmaf(f[i], p.c, -ref)), pb = ex2(fmaf(f[i + 1], p.c, -ref));
-              sum[i & 2] += pa;
-              sum[(i & 2) + 1] += pb;
-              x[i >> 1] = Half<T>::pack(pa, pb);
+              for (int i = 0; i < 32; ++i) x[i] = 0;
+              tmem_st32(ts, x);
+              tmem_st32(ts + 32, x);
+              tmem_wait_st();
+              tc_before();
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st32(ts, x);
-            tmem_st32(ts + 32, x + 32);
-            tmem_wait_st();
-            tc_before();
+            mbar_arrive(b_pready + 16 * st);
+            mbar_arrive(b_pready + 16 * st + 8);
           }
-          mbar_arrive(b_pready + 8 * st);
         }
         if (w.last()) {
-          // ------------------------------------------- the segment's end --
-          const int steps = w.steps();
-          const bool mine = q.dual || steps >= 2 || (n & 1) == st;   // this stream took part
-          const bool both = !q.dual && steps >= 2;
-          const bool owner = q.dual || (n & 1) == st;
-          float m2 = -INFINITY, l2 = 0.0f;
-          if (mine && !owner) {
-            // hand (m, l) over; the other group reads O.  Its reading of the
-            // last hand-over is behind the o_free of that segment.
-            if (on[st] > 0) ok = wait(s, b_ofree + 8 * st, (on[st] - 1) & 1, p);
+          // ----------------------------------------------- the run's end --
+          const bool took = w.total >= 2 || (n & 1) == st;   // this stream took part
+          if (took) {
+            ok = wait(s, b_ofull + 8 * st, on[st] & 1, p);
             if (!__all_sync(kFull, ok)) {
               ok = false;
               break;
             }
-            s.ml[r] = make_float2(m, l);
-            mbar_arrive(b_ml + 8 * st);
           }
-          if (owner) {
-            ok = ok && wait(s, b_ofull + 8 * st, on[st] & 1, p);
-            if (both) {
-              ok = ok && wait(s, b_ofull + 8 * (st ^ 1), on[st ^ 1] & 1, p);
-              ok = ok && wait(s, b_ml + 8 * (st ^ 1), mln[st ^ 1] & 1, p);
-              if (ok) {
-                const float2 t = s.ml[r];
-                m2 = t.x;
-                l2 = t.y;
-              }
+          if (__any_sync(kFull, slot != -2)) {
+            float* dst = nullptr;
+            if (slot != -2) {
+              const int b = q.b0 + (w.dual ? st * p.MB : 0) + j, hq = q.head * p.G + r % p.G;
+              const size_t row = slot >= 0 ? ((size_t)slot * 2 + st) * kRows + r
+                                           : whole_row(p, q.own ? 1 : 0, w.dual ? 0 : st, b, hq);
+              dst = p.part + row * HD;
+              // without a step of its own the stream has seen nothing, and O is not its
+              p.part_ml[row] = make_float2((m == -INFINITY ? 0.0f : m) - Half<T>::kShift, took ? l : 0.0f);
             }
-            if (!__all_sync(kFull, ok)) {
-              ok = false;
-              break;
-            }
-            if (busy) {
+            if (took) {
               tc_after();
-              const float mm = fmaxf(m, m2);
-              const float f1 = m == mm ? 1.0f : ex2(m - mm), f2 = m2 == -INFINITY ? 0.0f : ex2(m2 - mm);
-              float* dst = nullptr;
-              if (real) {
-                const int j = r / p.G, e = (q.dual ? st * p.MB : 0) + j;
-                const int b = q.b0 + e, hq = q.head * p.G + r % p.G;
-                const size_t row = q.slot >= 0
-                                       ? ((size_t)q.slot * 2 + (q.dual ? st : 0)) * kRows + r
-                                       : (size_t)p.n_slots * 2 * kRows +
-                                             ((size_t)(-1 - q.slot) * p.B + b) * p.Hq + hq;
-                dst = p.part + row * HD;
-                p.part_ml[row] = make_float2((mm == -INFINITY ? 0.0f : mm) - Half<T>::kShift,
-                                             l * f1 + l2 * f2);
-              }
 #pragma unroll 1
               for (int i = 0; i < HD; i += 32) {
                 uint32_t o[32];
                 tmem_ld32(tm_o[st] + lanes + i, o);
-                tmem_wait_ld();
-                float* of = reinterpret_cast<float*>(o);
-#pragma unroll
-                for (int k2 = 0; k2 < 32; ++k2) of[k2] *= f1;
-                if (both) {
-                  uint32_t o2[32];
-                  tmem_ld32(tm_o[st ^ 1] + lanes + i, o2);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int k2 = 0; k2 < 32; ++k2) of[k2] = fmaf(__uint_as_float(o2[k2]), f2, of[k2]);
-                }
-                if (real) {
+                tmem_wait_ld32(o);
+                if (slot != -2) {
 #pragma unroll
                   for (int k2 = 0; k2 < 32; k2 += 4)
-                    *reinterpret_cast<float4*>(dst + i + k2) =
-                        make_float4(of[k2], of[k2 + 1], of[k2 + 2], of[k2 + 3]);
+                    *reinterpret_cast<uint4*>(dst + i + k2) =
+                        make_uint4(o[k2], o[k2 + 1], o[k2 + 2], o[k2 + 3]);
                 }
               }
               tc_before();
             }
-            mbar_arrive(b_ofree + 8 * st);
-            if (both) mbar_arrive(b_ofree + 8 * (st ^ 1));
           }
+          if (took) mbar_arrive(b_ofree + 8 * st);
           // both groups keep both streams' counts
-          for (int t = 0; t < 2; ++t) {
-            const bool took = q.dual || steps >= 2 || (n & 1) == t;
-            if (took) on[t] += 1;
-            if (both && (n & 1) != t) mln[t] += 1;
-          }
+          for (int t = 0; t < 2; ++t)
+            if (w.total >= 2 || (n & 1) == t) on[t] += 1;
         }
         w.next();
       }
@@ -963,7 +1161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     ok = ok && *(volatile int*)&s.abort == 0;
-    if (!ok || skip + kMaxSegments >= s.total_seg) break;
+    if (!ok || skip + kMaxItems >= n_all) break;
     __syncthreads();
   }
 
@@ -981,39 +1179,100 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds up a row's partial results: prefix shares, then shares of its own
-// tokens, in the order of their blocks.  One warp per (entry, query head),
-// HD / 32 columns per lane.
+// Row (b, hq) from its own tokens alone, one warp, HD / 32 columns per lane:
+// what the tiles gave is not finite.  Slow, and right whatever the memory of
+// other entries holds.
 template <typename T, int HD>
+__device__ __noinline__ void row_alone(const AttnParams& p, int b, int hq, int group, float* acc, float* m_out,
+                                       float* l_out) {
+  constexpr int C = HD / 32;
+  const int lane = threadIdx.x & 31, h = hq / p.G;
+  const int limit = p.max_pages * kPageTokens;
+  const int lead = __ldg(p.group_start + group), pos = __ldg(p.positions + b);
+  const int prefix = min(max(__ldg(p.prefix_lens + group), 0), limit);
+  const int seen = pos < 0 || pos >= limit ? 0 : pos + 1;
+  const T* q = static_cast<const T*>(p.q) + (size_t)b * p.q_stride + (size_t)hq * HD + lane * C;
+  float qv[C], m = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    qv[i] = to_float(q[i]);
+    acc[i] = 0.0f;
+  }
+  for (int t = 0; t < seen; ++t) {
+    const int row = t < prefix ? lead : b;
+    const int id = __ldg(p.page_table + (size_t)row * p.max_pages + t / kPageTokens);
+    const bool there = id >= 0 && id < p.n_pages;
+    const size_t at = (((size_t)(there ? id : 0) * p.Hkv + h) * kPageTokens + t % kPageTokens) * HD + lane * C;
+    const T* k = static_cast<const T*>(p.k_pool) + at;
+    const T* v = static_cast<const T*>(p.v_pool) + at;
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) dot = fmaf(qv[i], there ? to_float(k[i]) : 0.0f, dot);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+    const float s = dot * p.c;
+    const float mn = fmaxf(m, s);
+    const float f = m == mn ? 1.0f : ex2(m - mn), w = s == -INFINITY ? 0.0f : ex2(s - mn);
+    m = mn;
+    l = fmaf(l, f, w);
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] = fmaf(w, there ? to_float(v[i]) : 0.0f, acc[i] * f);
+  }
+  *m_out = m;
+  *l_out = l;
+}
+
+// Adds up a row's partial results: prefix shares, then shares of its own
+// tokens, in a fixed order.  W warps per (entry, query head), HD / 32 columns
+// per lane.
+template <typename T, int HD, int W>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int C = HD / 32;
-  const int row = (int)((blockIdx.x * 128u + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= p.B * p.Hq) return;
+  __shared__ float s_acc[4][HD];
+  __shared__ float2 s_ml[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % W;
+  const int row = (int)blockIdx.x * (4 / W) + warp / W;
   const int b = row / p.Hq, hq = row % p.Hq, h = hq / p.G;
-  const Table tab{p.tab, p.B};
-  const int lead = tab.leader(b);
-  if (lead < 0) return;
-  const long long total = tab.total(), blocks = tab.blocks();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (row >= p.B * p.Hq) return;
+  const Entry e = p.entries[b];
+  if (e.lead < 0) return;
+  const Line line(reinterpret_cast<const int*>(p.entries + p.B)[0], p.grid);
   float acc[C], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int i = 0; i < C; ++i) acc[i] = 0.0f;
+#pragma unroll 1
   for (int kind = 0; kind < 2; ++kind) {
-    const int nt = kind == 0 ? tab.prefix_tiles(lead) : tab.own_tiles(b);
+    const int nt = kind == 0 ? e.prefix_tiles : e.own_tiles;
     if (nt == 0) continue;
-    const long long at = (kind == 0 ? tab.prefix_at(lead) : tab.own_at(b)) + (long long)h * nt;
-    const int c0 = block_of(at, total, blocks), c1 = block_of(at + nt - 1, total, blocks);
+    const bool dual = kind == 0 && e.prefix_width == 2;
+    const int w = dual ? 2 : 1;
+    const int at = kind == 0 ? e.prefix_at + h * nt * w : e.own_at + h * e.own_stride;
+    const int c0 = line.block_of(at), c1 = line.block_of(at + w * (nt - 1));
+    const bool whole = c0 == c1;
     // the row's place among its unit's rows
-    const int j = kind == 0 ? b - lead : 0;
-    const int stream = j / p.MB, r = (j % p.MB) * p.G + hq % p.G;
-    for (int c = c0; c <= c1; c += 32) {
-      // lane i looks at block c + i's share
-      const int n = min(32, c1 - c + 1), mine = c + min(lane, n - 1);
-      const size_t at_row =
-          c0 == c1 ? (size_t)p.n_slots * 2 * kRows + ((size_t)kind * p.B + b) * p.Hq + hq
-                   : ((size_t)(2 * mine + (mine == c0 ? 1 : 0)) * 2 + stream) * kRows + r;
-      const float2 ml = p.part_ml[at_row];
-      // a share that saw nothing has l = 0 (and O = 0): no weight
+    const int j = kind == 0 ? b - e.lead : b;
+    const int half = dual ? j / p.MB : 0, r = (j % p.MB) * p.G + hq % p.G;
+    const int n = (c1 - c0 + 1) * (dual ? 1 : 2);
+    for (int i0 = sub; i0 < n; i0 += 32 * W) {
+      // lane i looks at share i0 + W i: of a block, and of one of its streams
+      const int x = i0 + W * lane;
+      const int c = c0 + (dual ? x : x >> 1), stream = dual ? half : x & 1;
+      size_t at_row = 0;
+      float2 ml = make_float2(0.0f, 0.0f);
+      bool some = x < n;
+      if (some && dual && !whole) {
+        // a stretch of one step may hold no tile of two
+        const int t0 = max(0, (line.start(c) - at + 1) >> 1), t1 = min(nt, (line.start(c + 1) - at + 1) >> 1);
+        some = t0 < t1;
+      }
+      if (some) {
+        at_row = whole ? whole_row(p, kind, dual ? 0 : stream, b, hq)
+                       : ((size_t)(2 * c + (c == c0 ? 1 : 0)) * 2 + stream) * kRows + r;
+        ml = p.part_ml[at_row];
+      }
+      // a share that saw nothing has no weight, and its O is not looked at
       float top = ml.y == 0.0f ? -INFINITY : ml.x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
@@ -1024,11 +1283,13 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
       l *= fo;
 #pragma unroll
       for (int i = 0; i < C; ++i) acc[i] *= fo;
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
+      const int shares = min(32, (n - i0 + W - 1) / W);
+#pragma unroll 4
+      for (int i = 0; i < shares; ++i) {
         const float fi = __shfl_sync(kFull, f, i);
         l = fmaf(__shfl_sync(kFull, ml.y, i), fi, l);
         const float* src = p.part + __shfl_sync(kFull, (unsigned long long)at_row, i) * HD + lane * C;
+        if (fi == 0.0f) continue;
         if constexpr (C == 4) {
           const float4 v = *reinterpret_cast<const float4*>(src);
           acc[0] = fmaf(v.x, fi, acc[0]);
@@ -1043,6 +1304,33 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
       }
     }
   }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) s_acc[warp][lane * C + i] = acc[i];
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (sub != 0) return;
+    float mn = m;
+#pragma unroll
+    for (int k = 1; k < W; ++k) mn = fmaxf(mn, s_ml[warp + k].x);
+    const float f0 = m == mn ? 1.0f : ex2(m - mn);
+    l *= f0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] *= f0;
+#pragma unroll
+    for (int k = 1; k < W; ++k) {
+      const float2 ml = s_ml[warp + k];
+      const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - mn);
+      l = fmaf(ml.y, f, l);
+#pragma unroll
+      for (int i = 0; i < C; ++i) acc[i] = fmaf(s_acc[warp + k][lane * C + i], f, acc[i]);
+    }
+    m = mn;
+  }
+  float size = 0.0f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) size += fabsf(acc[i]);
+  if (__any_sync(kFull, !(size < INFINITY) || !(l < INFINITY))) row_alone<T, HD>(p, b, hq, e.group, acc, &m, &l);
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays
   uint32_t o[C / 2];
 #pragma unroll
@@ -1050,9 +1338,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + (size_t)row * HD + lane * C);
 #pragma unroll
   for (int i = 0; i < C / 2; ++i) out[i] = o[i];
-  if (p.lse && lane == 0) {
-    p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-  }
+  if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -1090,12 +1376,16 @@ int sm_count(int device) {
   return count[device];
 }
 
+// Rows up to which four warps join one: few rows have many shares each.
+constexpr unsigned kWideJoin = 2048;
+
 constexpr int kMaxBlocks = 160;      // at least the device's multiprocessors
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// Split shares: two per block and stream; whole units: two kinds and streams.
 size_t part_rows(const mk_prefix_attention_args* a) {
-  return (size_t)2 * kMaxBlocks * 2 * kRows + (size_t)2 * a->batch * a->n_q_heads;
+  return (size_t)2 * kMaxBlocks * 2 * kRows + (size_t)4 * a->batch * a->n_q_heads;
 }
 
 mk_status validate(const mk_prefix_attention_args* a) {
@@ -1108,30 +1398,42 @@ mk_status validate(const mk_prefix_attention_args* a) {
   if (a->batch > kMaxBatch || a->n_groups > kMaxBatch) return MK_ERR_CAPACITY;
   if (a->n_q_heads / a->n_kv_heads > kMaxGroup || a->n_q_heads > (1 << 16)) return MK_ERR_CAPACITY;
   if (a->max_pages > (INT32_MAX - kTile) / kPageTokens) return MK_ERR_CAPACITY;
-  // row numbers of the pools' tensor maps are 32-bit
+  // places in the line of tiles are 32-bit, and so are row numbers of the pools' tensor maps
+  if ((long long)a->batch * a->n_kv_heads * ((long long)a->max_pages + 4) > INT32_MAX) return MK_ERR_CAPACITY;
   if (((long long)a->n_pages + 1) * a->n_kv_heads * kPageTokens > INT32_MAX) return MK_ERR_CAPACITY;
   return MK_OK;
 }
 
-template <typename T, int HD>
-cudaError_t launch_attention(const AttnParams& p, const CUtensorMap* maps, int blocks, cudaStream_t st) {
-  using L = Layout<HD>;
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<T, HD>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDyn);
-  if (e != cudaSuccess) return e;
-  attention_kernel<T, HD><<<blocks, kThreads, L::kDyn, st>>>(p, maps[0], maps[1], maps[2], maps[3]);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+// Both launches may begin while the one ahead is finishing: they wait for it
+// before they touch memory.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t st,
+                   const A&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((p.B * p.Hq + 3) / 4));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, HD>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int HD>
+cudaError_t launch_attention(const AttnParams& p, const CUtensorMap* maps, cudaStream_t st) {
+  using L = Layout<HD>;
+  cudaError_t e = cudaFuncSetAttribute(attention_kernel<T, HD>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDyn);
+  if (e != cudaSuccess) return e;
+  e = launch(attention_kernel<T, HD>, (unsigned)p.grid, kThreads, L::kDyn, st, p, maps[0], maps[1], maps[2],
+             maps[3]);
+  if (e != cudaSuccess) return e;
+  const unsigned rows = (unsigned)(p.B * p.Hq);
+  if (rows <= kWideJoin) return launch(join_kernel<T, HD, 4>, rows, 128, 0, st, p);
+  return launch(join_kernel<T, HD, 1>, (rows + 3) / 4, 128, 0, st, p);
 }
 
 }  // namespace
@@ -1143,7 +1445,7 @@ extern "C" size_t mk_prefix_attention_workspace(const mk_prefix_attention_args* 
   if (validate(a) != MK_OK) return 0;
   const size_t rows = part_rows(a);
   return round256(rows * a->head_dim * sizeof(float)) + round256(rows * sizeof(float2)) +
-         round256(table_bytes(a->batch));
+         round256(sizeof(Entry) * (size_t)a->batch + sizeof(int));
 }
 
 extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* a, void* stream) {
@@ -1186,7 +1488,12 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* a, void
   w += round256(rows * a->head_dim * sizeof(float));
   p.part_ml = reinterpret_cast<float2*>(w);
   w += round256(rows * sizeof(float2));
-  p.tab = reinterpret_cast<long long*>(w);
+  p.entries = reinterpret_cast<Entry*>(w);
+  p.grid = blocks;
+  p.q = a->q;
+  p.k_pool = a->k_pool;
+  p.v_pool = a->v_pool;
+  p.q_stride = a->batch > 1 ? a->q_token_stride : row;
   p.n_slots = 2 * kMaxBlocks;
   p.out = a->out;
   p.lse = a->lse;
@@ -1207,9 +1514,8 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* a, void
   {
     // {64 columns, query heads, entries, chunks}: the heads of one KV head of
     // as many entries as a stream's rows hold, and of one
-    const long long ts = a->batch > 1 ? a->q_token_stride : row;
     const cuuint64_t dims[4] = {64, (cuuint64_t)a->n_q_heads, (cuuint64_t)a->batch, hd / 64};
-    const cuuint64_t strides[3] = {hd * 2, (cuuint64_t)ts * 2, 128};
+    const cuuint64_t strides[3] = {hd * 2, (cuuint64_t)p.q_stride * 2, 128};
     cuuint32_t box[4] = {64, (cuuint32_t)p.G, (cuuint32_t)p.MB, 1};
     if (!encode(&maps[2], type, 4, a->q, dims, strides, box)) return MK_ERR_INVALID;
     box[2] = 1;
@@ -1218,10 +1524,10 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* a, void
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a->type == MK_BF16)
-    e = a->head_dim == 128 ? launch_attention<__nv_bfloat16, 128>(p, maps, blocks, st)
-                           : launch_attention<__nv_bfloat16, 64>(p, maps, blocks, st);
+    e = a->head_dim == 128 ? launch_attention<__nv_bfloat16, 128>(p, maps, st)
+                           : launch_attention<__nv_bfloat16, 64>(p, maps, st);
   else
-    e = a->head_dim == 128 ? launch_attention<__half, 128>(p, maps, blocks, st)
-                           : launch_attention<__half, 64>(p, maps, blocks, st);
+    e = a->head_dim == 128 ? launch_attention<__half, 128>(p, maps, st)
+                           : launch_attention<__half, 64>(p, maps, st);
   return from_cuda(e);
 }
