@@ -9,22 +9,24 @@
 // into [-pi, pi] in 64 bits, since at position 2^18 one 32-bit rounding step
 // of the angle is already 2^-6; the sine and cosine are then 32-bit.
 //
-// Bound: memory (each row is read and written once, no reuse).  A block takes
-// kTokens tokens, forms their sines and cosines once for all heads in shared
-// memory, and each thread turns 16 columns of a head: two 16-byte loads and
-// two 16-byte stores for 16-bit rows, issued before the block waits for the
-// table.
+// Bound: memory (each row is read and written once, no reuse), and next to it
+// the instructions that turn the pairs.  A warp takes a token, or some heads of
+// one: it asks for all its rows first (16 columns a lane and head, two 16-byte
+// loads of 16-bit rows); while they are on their way it looks up the token's
+// place and forms its sines and cosines, two a lane, which a lane then holds in
+// registers for all its heads.  No warp waits for another.
 #include "ops_common.cuh"
 
 namespace mk {
 namespace ops {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
 
 struct AppendParams {
   int T, rows, max_pages, n_pages, Hq, Hkv, R;
-  int stage_q;               // query heads present (0: none)
+  int splits, rounds;        // warps of a token, and how many times each turns the heads it can at once
   float magnitude;
   const void *q, *k, *v;
   long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;   // strides in elements
@@ -34,147 +36,184 @@ struct AppendParams {
   int32_t* status;
 };
 
-// cos and sin of position * f: the angle less the nearest multiple of 2 pi,
-// the multiple subtracted in two parts (2 pi as a sum of two doubles).
+// cos and sin of position * f, times magnitude: the angle in turns, less the
+// nearest whole number, in 64 bits.
 __device__ __forceinline__ float2 turn(int position, double f, float magnitude) {
-  constexpr double kTwoPiHi = 6.283185307179586;         // 2 pi rounded to 53 bits
-  constexpr double kTwoPiLo = 2.4492935982947064e-16;    // 2 pi - kTwoPiHi
-  const double a = (double)position * f;
-  const double n = rint(a * 0.15915494309189535);        // 1 / (2 pi)
-  const float r = (float)fma(-n, kTwoPiLo, fma(-n, kTwoPiHi, a));
+  const double a = (double)position * f * 0.15915494309189535;   // 1 / (2 pi)
   float s, c;
-  sincosf(r, &s, &c);
+  sincospif((float)(2.0 * (a - rint(a))), &s, &c);
   return make_float2(c * magnitude, s * magnitude);
 }
 
-// 8 consecutive elements as floats; WIDE: the address is 16-byte aligned.
+// Rounds whose rows a lane holds at once: 8 registers each of 16-bit rows, 16
+// of 32-bit ones.  (8192 tokens of 24 heads of 128: 21.5 us with 6 rounds, 21.4
+// with 4, 21.1 with 2; a block of 256 threads that kept its tokens' sines in
+// shared memory for all heads took 27.1, with the next tokens' rows under way 27.6.)
+template <typename S>
+constexpr int kMostRounds = sizeof(S) == 4 ? 2 : 4;
+// Up to so many single rounds (32 warps on each of 148 multiprocessors) every
+// warp takes one: there is room for them, and the chain of a warp is shortest.
+constexpr long long kFewWarps = 148 * 32;
+
+// 16 elements as they lie in memory: two groups of 8.
+template <typename S>
+struct Raw {
+  uint4 w[sizeof(S)];
+};
+
 template <typename S, bool WIDE>
-__device__ __forceinline__ void load8(const S* p, float* f) {
-  if constexpr (!WIDE) {
+__device__ __forceinline__ void load8(const S* p, uint4* w) {
+  if constexpr (WIDE) {              // the address is 16-byte aligned
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = to_float(p[i]);
-  } else if constexpr (sizeof(S) == 4) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    for (int i = 0; i < (int)sizeof(S) / 2; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
   } else {
-    Vec8<S>::unpack(__ldg(reinterpret_cast<const uint4*>(p)), f);
+    S* e = reinterpret_cast<S*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = p[i];
+  }
+}
+template <typename S>
+__device__ __forceinline__ void unpack16(const Raw<S>& r, float* x) {
+  if constexpr (sizeof(S) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[4 * i] = __uint_as_float(r.w[i].x);
+      x[4 * i + 1] = __uint_as_float(r.w[i].y);
+      x[4 * i + 2] = __uint_as_float(r.w[i].z);
+      x[4 * i + 3] = __uint_as_float(r.w[i].w);
+    }
+  } else {
+    Vec8<S>::unpack(r.w[0], x);
+    Vec8<S>::unpack(r.w[1], x + 8);
   }
 }
 
-// MODE 0: half layout, R a multiple of 8: the thread's two groups of 8 columns
+// MODE 0: half layout, R a multiple of 8: the lane's two groups of 8 columns
 // are the two halves of its 8 pairs.  MODE 1: interleaved: 16 consecutive
-// columns.  MODE 2: half layout, any R: 16 consecutive columns whose partners
-// are read back from the row staged in shared memory.
+// columns.  MODE 2: half layout, any R: 16 consecutive columns whose partners,
+// held by other lanes, are exchanged through shared memory.
 template <typename S, typename D, int HD, int MODE, bool WIDE>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const AppendParams p, int tokens) {
-  extern __shared__ float2 s_tab[];          // [tokens][R], then MODE 2's rows
-  constexpr int PER_HEAD = HD / 16;
-  const int R = p.R;
-  const int heads = p.stage_q + 2 * p.Hkv;
-  const int t0 = blockIdx.x * tokens;
-  const int nt = min(tokens, p.T - t0);
-  const int items = nt * heads * PER_HEAD;
-  float* rows = reinterpret_cast<float*>(s_tab + (size_t)tokens * R);
-
-  for (int i = threadIdx.x; i < nt * R; i += kThreads) {
-    const int t = i / R;
-    s_tab[i] = turn(__ldg(p.positions + t0 + t), __ldg(p.inv_freq + (i - t * R)), p.magnitude);
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int PER_HEAD = HD / 16;          // lanes of a head
+  constexpr int kHeads = 32 / PER_HEAD;      // heads that a warp turns at once
+  constexpr int kAhead = kMostRounds<S>;
+  // cos and sin of pair i; for MODE 0 and 1 the two of pairs 8 j + k, k even and
+  // odd, at place (k / 2) PER_HEAD + j, so that lanes j read without bank conflicts
+  __shared__ __align__(16) float2 s_tab[kWarps][HD / 2];
+  __shared__ float s_rows[kWarps][MODE == 2 ? 512 : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = p.R, heads = p.Hq + 2 * p.Hkv;
+  const long long unit = (long long)blockIdx.x * kWarps + warp;
+  const int t = (int)(unit / p.splits), part = (int)(unit - (long long)t * p.splits);
+  const int j = lane % PER_HEAD, h0 = part * p.rounds * kHeads + lane / PER_HEAD;
+  // where the lane's two groups of 8 columns start
+  auto columns = [&](int head, int* c0, int* c1) {
+    const bool paired = MODE == 0 && head < p.Hq + p.Hkv && 8 * j < R;
+    *c0 = paired ? 8 * j : 16 * j;
+    *c1 = paired ? R + 8 * j : 16 * j + 8;
+  };
+  // Nothing of the call's memory is touched before the kernels ahead are done.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (t >= p.T) return;
+  const int pos = __ldg(p.positions + t), seq = p.seq ? __ldg(p.seq + t) : t;
+  Raw<S> raw[kAhead];
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) {
+    const int head = h0 + a * kHeads;
+    if (a < p.rounds && head < heads) {
+      const S* src = head < p.Hq ? static_cast<const S*>(p.q) + t * p.q_ts + head * p.q_hs
+                     : head < p.Hq + p.Hkv
+                         ? static_cast<const S*>(p.k) + t * p.k_ts + (head - p.Hq) * p.k_hs
+                         : static_cast<const S*>(p.v) + t * p.v_ts + (head - p.Hq - p.Hkv) * p.v_hs;
+      int c0, c1;
+      columns(head, &c0, &c1);
+      load8<S, WIDE>(src + c0, raw[a].w);
+      load8<S, WIDE>(src + c1, raw[a].w + sizeof(S) / 2);
+    }
   }
-  for (int base = 0; base < items; base += kThreads) {
-    const int it = base + threadIdx.x;
-    const int j = it % PER_HEAD, hh = (it / PER_HEAD) % heads, t = t0 + it / (PER_HEAD * heads);
-    const bool in = it < items;
-    const bool is_v = hh >= p.stage_q + p.Hkv;
-    const bool is_q = hh < p.stage_q;
-    // where this thread's two groups of 8 columns start
-    const bool paired = MODE == 0 && !is_v && 8 * j < R;
-    const int c0 = paired ? 8 * j : 16 * j;
-    const int c1 = paired ? R + 8 * j : 16 * j + 8;
+  // the token's place: a negative sequence is padding
+  int page = -1;
+  if (seq >= p.rows) {
+    if (lane == 0) report(p.status, MK_ERR_DEVICE, MK_OP_ROPE_APPEND, t, seq, p.rows);
+  } else if (seq >= 0) {
+    if (pos < 0 || pos / kPageTokens >= p.max_pages) {
+      if (lane == 0) report(p.status, MK_ERR_DEVICE, MK_OP_ROPE_APPEND, t, pos, p.max_pages * kPageTokens);
+    } else {
+      page = __ldg(p.page_table + (size_t)seq * p.max_pages + pos / kPageTokens);
+      if (page < 0 || page >= p.n_pages) {
+        if (lane == 0) report(p.status, MK_ERR_DEVICE, MK_OP_ROPE_APPEND, t, page, p.n_pages);
+        page = -1;
+      }
+    }
+  }
+  if (page < 0) return;                      // the whole warp
+#pragma unroll
+  for (int i = lane; i < HD / 2; i += 32)
+    if (i < R) s_tab[warp][MODE == 2 ? i : (i % 8 / 2 * PER_HEAD + i / 8) * 2 + i % 2] = turn(pos, __ldg(p.inv_freq + i), p.magnitude);
+  __syncwarp();
+  float2 cs[MODE == 2 ? 1 : 8];
+  if constexpr (MODE != 2) {
+    if (8 * j < R) {
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const float4 two = reinterpret_cast<const float4*>(s_tab[warp])[k / 2 * PER_HEAD + j];
+        cs[k] = make_float2(two.x, two.y);
+        cs[k + 1] = make_float2(two.z, two.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) {
+    const int head = h0 + a * kHeads;
+    if (a >= p.rounds) break;                // the whole warp
+    const bool in = head < heads, is_v = head >= p.Hq + p.Hkv;
     float x[16];
-    if (in) {
-      const S* src = is_q   ? static_cast<const S*>(p.q) + t * p.q_ts + hh * p.q_hs
-                     : is_v ? static_cast<const S*>(p.v) + t * p.v_ts + (hh - p.stage_q - p.Hkv) * p.v_hs
-                            : static_cast<const S*>(p.k) + t * p.k_ts + (hh - p.stage_q) * p.k_hs;
-      load8<S, WIDE>(src + c0, x);
-      load8<S, WIDE>(src + c1, x + 8);
-    }
-    // the token's place: a negative sequence is padding, skipped
-    int page = -1, pos = 0, seq = -1;
-    if (in) {
-      pos = __ldg(p.positions + t);
-      seq = p.seq ? __ldg(p.seq + t) : t;
-      if (seq >= 0) {
-        if (seq >= p.rows) {
-          report(p.status, MK_ERR_DEVICE, MK_OP_ROPE_APPEND, t, seq, p.rows);
-        } else if (pos < 0 || pos / kPageTokens >= p.max_pages) {
-          report(p.status, MK_ERR_DEVICE, MK_OP_ROPE_APPEND, t, pos, p.max_pages * kPageTokens);
-        } else {
-          page = __ldg(p.page_table + (size_t)seq * p.max_pages + pos / kPageTokens);
-          if (page < 0 || page >= p.n_pages) {
-            report(p.status, MK_ERR_DEVICE, MK_OP_ROPE_APPEND, t, page, p.n_pages);
-            page = -1;
-          }
-        }
-      }
-    }
+    unpack16(raw[a], x);
     if constexpr (MODE == 2) {
-      if (base) __syncthreads();             // the previous rows have been read
-      if (in && !is_v) {
-        float* row = rows + threadIdx.x * 16;
+      __syncwarp();                          // the previous rows have been read
+      float* row = s_rows[warp] + lane * 16;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) row[i] = x[i];
-      }
+      for (int k = 0; k < 16; ++k) row[k] = x[k];
+      __syncwarp();
     }
-    if (base == 0 || MODE == 2) __syncthreads();   // the table (and the staged rows) are written
-    if (page < 0) continue;
+    if (!in) continue;
+    int c0, c1;
+    columns(head, &c0, &c1);
     if (!is_v) {
-      const float2* tab = s_tab + (t - t0) * R;
-      if constexpr (MODE == 0) {
-        if (paired) {
+      if constexpr (MODE == 2) {
+        const float* row = s_rows[warp] + (lane - j) * 16;   // the head's
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 cs = tab[8 * j + i];
-            const float a = x[i], b = x[8 + i];
-            x[i] = a * cs.x - b * cs.y;
-            x[8 + i] = b * cs.x + a * cs.y;
-          }
-        }
-      } else if constexpr (MODE == 1) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (8 * j + i < R) {
-            const float2 cs = tab[8 * j + i];
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * cs.x - b * cs.y;
-            x[2 * i + 1] = b * cs.x + a * cs.y;
-          }
-        }
-      } else {
-        // a head's items are consecutive threads of one block, HD / 16 a
-        // power of two, so the head's row starts at this thread less j
-        const float* row = rows + (threadIdx.x - j) * 16;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int c = 16 * j + i;
+        for (int k = 0; k < 16; ++k) {
+          const int c = 16 * j + k;
           if (c < R) {
-            const float2 cs = tab[c];
-            x[i] = x[i] * cs.x - row[c + R] * cs.y;
+            const float2 w = s_tab[warp][c];
+            x[k] = x[k] * w.x - row[c + R] * w.y;
           } else if (c < 2 * R) {
-            const float2 cs = tab[c - R];
-            x[i] = x[i] * cs.x + row[c - R] * cs.y;
+            const float2 w = s_tab[warp][c - R];
+            x[k] = x[k] * w.x + row[c - R] * w.y;
+          }
+        }
+      } else if (8 * j < R) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float& lo = MODE == 0 ? x[k] : x[2 * k];
+          float& hi = MODE == 0 ? x[8 + k] : x[2 * k + 1];
+          if (MODE == 0 || 8 * j + k < R) {
+            const float a0 = lo, b0 = hi;
+            lo = a0 * cs[k].x - b0 * cs[k].y;
+            hi = b0 * cs[k].x + a0 * cs[k].y;
           }
         }
       }
     }
     D* dst;
-    if (is_q) {
-      dst = static_cast<D*>(p.q_out) + ((size_t)t * p.Hq + hh) * HD;
+    if (head < p.Hq) {
+      dst = static_cast<D*>(p.q_out) + ((size_t)t * p.Hq + head) * HD;
     } else {
-      const int h = is_v ? hh - p.stage_q - p.Hkv : hh - p.stage_q;
+      const int h = is_v ? head - p.Hq - p.Hkv : head - p.Hq;
       dst = static_cast<D*>(is_v ? p.v_pool : p.k_pool) +
-            (((size_t)page * p.Hkv + h) * kPageTokens + pos % kPageTokens) * HD;
+            (((size_t)page * p.Hkv + h) * kPageTokens + (pos & (kPageTokens - 1))) * HD;
     }
     *reinterpret_cast<uint4*>(dst + c0) = Vec8<D>::pack(x);
     *reinterpret_cast<uint4*>(dst + c1) = Vec8<D>::pack(x + 8);
@@ -182,13 +221,24 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const AppendParam
 }
 
 template <typename S, typename D, int HD, int MODE, bool WIDE>
-cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
-  const int tokens = 1;
-  const size_t smem = (size_t)tokens * p.R * sizeof(float2) +
-                      (MODE == 2 ? (size_t)kThreads * 16 * sizeof(float) : 0);
-  rope_append_kernel<S, D, HD, MODE, WIDE>
-      <<<(p.T + tokens - 1) / tokens, kThreads, smem, stream>>>(p, tokens);
-  return cudaGetLastError();
+cudaError_t launch(AppendParams p, cudaStream_t stream) {
+  // A warp takes all heads of a token, as far as its registers hold them; while
+  // that gives the device fewer warps than it can run, as few as it turns at once.
+  constexpr int kHeads = 32 / (HD / 16);
+  const int rounds = (p.Hq + 2 * p.Hkv + kHeads - 1) / kHeads;
+  p.splits = (long long)p.T * rounds <= kFewWarps ? rounds : (rounds + kMostRounds<S> - 1) / kMostRounds<S>;
+  p.rounds = (rounds + p.splits - 1) / p.splits;
+  const long long units = (long long)p.T * p.splits;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((units + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_append_kernel<S, D, HD, MODE, WIDE>, (const AppendParams)p);
 }
 
 template <typename S, typename D, int HD, int MODE>
@@ -252,7 +302,6 @@ extern "C" mk_status mk_rope_append(const mk_rope_append_args* a, void* stream) 
   p.Hq = a->n_q_heads;
   p.Hkv = a->n_kv_heads;
   p.R = a->rotary_dim / 2;
-  p.stage_q = a->n_q_heads;
   p.magnitude = a->magnitude;
   p.q = a->q; p.k = a->k; p.v = a->v;
   p.q_ts = a->q_token_stride; p.q_hs = a->q_head_stride;

@@ -22,10 +22,11 @@
 // graph replays with new ones.  A block's share of a unit leaves partial
 // results (O, m, l); a second launch adds them up.
 //
-// One block: a TMA warp streams K and V tiles, a warp issues tcgen05 MMAs,
+// One block: a TMA warp streams K and V tiles, two warps issue tcgen05 MMAs,
 // and two groups of four warps hold a softmax row per thread.  S = Q K^T and O
 // live in tensor memory, two of each ("streams"), so that one stream's softmax
-// runs under the other's MMAs.  With more than 128 rows the streams are the
+// runs under the other's MMAs.  Each stream has its own MMA warp, since one
+// warp's instructions between two MMAs left the pipe idle.  With more than 128 rows the streams are the
 // two tiles of rows, and each K and V tile serves both; with fewer they are
 // alternate tiles of tokens of the same rows, two partial results.  P goes
 // back to tensor memory over S and is the A operand of P V.
@@ -48,10 +49,10 @@ namespace {
 constexpr int kRows = 128;           // query rows of a stream
 constexpr int kTile = 128;           // tokens of a K or V tile
 constexpr int kGroupThreads = 128;   // a softmax group: one row per thread
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;   // one MMA warp per stream
+constexpr int kThreads = 352;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxItems = 48;        // of one pass of a block over its stretch
+constexpr int kMaxItems = 32;        // of one pass of a block over its stretch; a power of two
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroup = 64;        // query heads per KV head
 constexpr float kRescale = 8.0f;     // log2 of the growth that O may lag behind
@@ -208,28 +209,46 @@ __device__ __forceinline__ void tc_before() {
 __device__ __forceinline__ void tc_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// The following are run by a whole warp and issued by one elected lane: in
+// code that only one lane reaches, the operands would have to be moved to
+// uniform registers before each instruction (measured: 85 cycles an MMA).
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   bar)
-               : "memory");
-}
-// D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem], four steps of 16 along K: 32 bytes of a row each
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc) {
+// D[tmem] (+)= A[tmem] B[smem], four steps of 16 along K: 8 columns of A, 16
+// rows of 128 bytes of B each
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+      "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
@@ -261,15 +280,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 }
 #undef MK_R4
 #undef MK_I4
-#define MK_W8(r, i)                                                                            \
-  "+r"((r)[i]), "+r"((r)[(i) + 1]), "+r"((r)[(i) + 2]), "+r"((r)[(i) + 3]), "+r"((r)[(i) + 4]), \
-      "+r"((r)[(i) + 5]), "+r"((r)[(i) + 6]), "+r"((r)[(i) + 7])
-// Tied to the registers of the load, so that no use of them moves up.
+#define MK_W4(r, i) "+r"((r)[i]), "+r"((r)[(i) + 1]), "+r"((r)[(i) + 2]), "+r"((r)[(i) + 3])
+#define MK_W16(r, i) MK_W4(r, i), MK_W4(r, (i) + 4), MK_W4(r, (i) + 8), MK_W4(r, (i) + 12)
+// Waits for loads; tied to their registers, so that no use of these moves up.
 __device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : MK_W8(r, 0), MK_W8(r, 8), MK_W8(r, 16), MK_W8(r, 24)::"memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : MK_W16(r, 0), MK_W16(r, 16)::"memory");
 }
-#undef MK_W8
+#undef MK_W4
+#undef MK_W16
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -288,13 +306,14 @@ struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_ready[4];    // p_ready: two halves of a tile's tokens per stream
   uint64_t o_full[2], o_free[2];
+  uint64_t turn[2];                  // the other stream has taken its exponentials
 };
 
 struct Block {
   Bars bars;
-  Item items[kMaxItems];
+  Item items[kMaxItems];             // unit u in place u mod kMaxItems
   int scan[kWarps][4];
-  int first, last;                   // units of the block's stretch
+  unsigned first, last;              // units of the block's stretch
   int win_lo, win_hi;                // stretch of this pass
   int n_steps;
   uint32_t tmem;
@@ -328,25 +347,23 @@ __device__ __forceinline__ bool wait(Block& s, uint32_t bar, uint32_t parity, co
 // for each n V of step n and K of step n + 2.
 struct Walk {
   const Item* items;
-  int n;
+  int n, base;                       // items, unit of the first
   int i = 0, j = 0, run = 0;         // item, step of it, run
   int count = 0, j0 = 0, total = 0;  // the item's steps, those of the run before it and in all
   bool dual = false;
-  __device__ __forceinline__ Walk(const Item* it, int n_items) : items(it), n(n_items) { enter(); }
+  __device__ __forceinline__ Walk(const Item* it, int n_items, int first) : items(it), n(n_items), base(first) {
+    enter();
+  }
   __device__ __forceinline__ void enter() {
     if (i >= n) return;
-    const Item& q = items[i];
+    const Item& q = at();
     dual = q.dual;
     count = (q.t1 - q.t0) << (dual ? 1 : 0);
     j0 = q.j0;
     total = q.steps;
   }
-  __device__ __forceinline__ bool done() const { return i >= n; }
-  __device__ __forceinline__ const Item& at() const { return items[i]; }
-  __device__ __forceinline__ int tile() const { return items[i].t0 + (dual ? j >> 1 : j); }
+  __device__ __forceinline__ const Item& at() const { return items[(base + i) % kMaxItems]; }
   __device__ __forceinline__ bool loads() const { return !(dual && (j & 1)); }   // a new tile
-  __device__ __forceinline__ bool frees() const { return !dual || (j & 1); }     // its last use
-  __device__ __forceinline__ bool enters() const { return j == 0; }
   __device__ __forceinline__ bool first() const { return j0 + j == 0; }          // of the run
   __device__ __forceinline__ bool last() const { return j0 + j == total - 1; }
   __device__ __forceinline__ bool first_of_stream() const { return j0 + j < 2; }
@@ -403,9 +420,9 @@ static_assert(list_words(kMaxBatch, kMaxBatch) * 4 <= Layout<128>::kDyn - Layout
               "the list's scratch does not fit the ring");
 
 // Fills s.items with items [skip, skip + kMaxItems) of this block's stretch;
-// returns how many there are in all.  `tmp` is list_words of shared memory,
+// returns how many there are in all, and the unit of the pass's first.  `tmp` is list_words of shared memory,
 // idle now.
-__device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip) {
+__device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip, int* first) {
   const int n = p.n_groups, B = p.B;
   int32_t* gs = tmp;                               // [n + 1]
   int32_t* pl = gs + n + 1;                        // [n]
@@ -441,7 +458,7 @@ __device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip)
   }
   if (threadIdx.x == 0) {
     s.first = INT32_MAX;
-    s.last = -1;
+    s.last = 0;
     s.n_steps = 0;
   }
   bad = __syncthreads_or(bad);
@@ -562,31 +579,11 @@ __device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip)
       }
     }
   };
-  visit([&](bool, int, int, int, int, int, int, int unit) {
-    atomicMin(&s.first, unit);
-    atomicMax(&s.last, unit);
-  });
-  __syncthreads();
-  const int first = s.first + skip;
-  const int n_items = s.last < 0 ? 0 : s.last - s.first + 1;
-  if (n_items > kMaxItems) {         // more than one pass: the runs end with a pass
-    if (threadIdx.x == 0) {
-      s.win_lo = r0;
-      s.win_hi = r1;
-    }
-    __syncthreads();
-    visit([&](bool, int, int, int us, int, int t0, int, int unit) {
-      if (unit == first) s.win_lo = us + t0;
-      if (unit == first + kMaxItems) s.win_hi = us;
-    });
-    __syncthreads();
-    r0 = max(r0, s.win_lo);
-    r1 = min(r1, s.win_hi);
-  }
-  visit([&](bool prefix, int b, int h, int us, int nt, int t0, int t1, int unit) {
-    if (unit < first || unit >= first + kMaxItems) return;
+  // `keep` says which units to write; their place needs no count of those before
+  auto write = [&](auto&& keep) { visit([&](bool prefix, int b, int h, int us, int nt, int t0, int t1, int unit) {
+    if (!keep(unit)) return;
     const int g = group[b];
-    Item& q = s.items[unit - first];
+    Item& q = s.items[unit % kMaxItems];
     q.head = h;
     q.t0 = t0;
     q.t1 = t1;
@@ -618,16 +615,36 @@ __device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip)
     }
     const bool whole = t0 == 0 && t1 == nt;
     q.slot = (short)(whole ? -1 : 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0));
+  }); };
+  write([&](int unit) {
+    atomicMin(&s.first, (unsigned)unit);
+    atomicMax(&s.last, (unsigned)unit + 1u);
+    return true;
   });
   __syncthreads();
+  *first = (int)s.first + skip;
+  const int n_items = s.last == 0 ? 0 : (int)(s.last - s.first);
+  if (n_items > kMaxItems) {         // more than one pass: the runs end with a pass
+    const int from = *first;
+    if (threadIdx.x == 0) {
+      s.win_lo = r0;
+      s.win_hi = r1;
+      s.n_steps = 0;
+    }
+    __syncthreads();
+    visit([&](bool, int, int, int us, int, int t0, int, int unit) {
+      if (unit == from) s.win_lo = us + t0;
+      if (unit == from + kMaxItems) s.win_hi = us;
+    });
+    __syncthreads();
+    r0 = max(r0, s.win_lo);
+    r1 = min(r1, s.win_hi);
+    write([&](int unit) { return unit >= from && unit < from + kMaxItems; });
+    __syncthreads();
+  }
   return n_items;
 }
 
-// Whether a tile has tokens inside its loaded pages that are not the unit's:
-// what lies there is not the sequence's, and 0 x infinity would spoil the row.
-__device__ __forceinline__ bool ragged(const Item& q, int at) {
-  return at < q.lo || (at + kTile > q.hi && (q.hi & (kPageTokens - 1)) != 0);
-}
 __device__ __forceinline__ int first_token(const Item& q, int tile) {
   return q.lo / kPageTokens * kPageTokens + tile * kTile;
 }
@@ -680,7 +697,7 @@ __device__ __forceinline__ uint64_t exp2_pair(uint64_t y) {
 
 // Pairs of every 16 whose exponentials the FMA pipe takes over from the
 // special-function unit, which alone would bound the softmax.
-constexpr int kFmaPairs = 6;
+constexpr int kFmaPairs = 0;
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -695,19 +712,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t b_full = saddr(s.bars.full), b_empty = saddr(s.bars.empty);
   const uint32_t b_qfull = saddr(s.bars.q_full), b_qempty = saddr(s.bars.q_empty);
   const uint32_t b_sfull = saddr(s.bars.s_full), b_pready = saddr(s.bars.p_ready);
+  const uint32_t b_turn = saddr(s.bars.turn);
   const uint32_t b_ofull = saddr(s.bars.o_full), b_ofree = saddr(s.bars.o_free);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(b_full + 8 * i, 1);
-      mbar_init(b_empty + 8 * i, 1);
+      mbar_init(b_empty + 8 * i, 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_qfull + 8 * i, 1);
-      mbar_init(b_qempty + 8 * i, 1);
+      mbar_init(b_qempty + 8 * i, 2);
       mbar_init(b_sfull + 8 * i, 1);
       mbar_init(b_pready + 16 * i, kGroupThreads);
       mbar_init(b_pready + 16 * i + 8, kGroupThreads);
+      mbar_init(b_turn + 8 * i, kGroupThreads / 32);
       mbar_init(b_ofull + 8 * i, 1);
       mbar_init(b_ofree + 8 * i, kGroupThreads);
     }
@@ -731,15 +750,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Barrier use counts, carried from pass to pass by every role that needs them.
+  // (No arrays: one whose index is not known when compiling would lie in memory,
+  // and next to this much shared memory there is no L1 cache for it.)
   uint32_t ring = 0;                 // tiles loaded so far
-  uint32_t qn[2] = {0, 0};           // uses of each query slot
-  uint32_t sn[2] = {0, 0};           // steps of each stream
-  uint32_t on[2] = {0, 0};           // runs of each stream
+  uint32_t q0_uses = 0, q1_uses = 0; // of the query slots
+  uint32_t sn = 0, on = 0;           // steps and runs of the warp's stream
+  uint32_t turns = 0;                // steps of the other stream
   bool ok = true;
   uint32_t tm = 0;
 
   for (int skip = 0;; skip += kMaxItems) {
-    const int n_all = list_items(s, p, reinterpret_cast<int32_t*>(base + L::kRing), skip);
+    int first;
+    const int n_all = list_items(s, p, reinterpret_cast<int32_t*>(base + L::kRing), skip, &first);
     const int n_items = min(kMaxItems, n_all - skip), n_steps = s.n_steps;
     // the list's scratch is the ring: later writes there go through TMA
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -747,7 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_after();
     tm = s.tmem;
-    const uint32_t tm_s[2] = {tm, tm + 128}, tm_o[2] = {tm + 256, tm + 384};
+    const int st = warp < kTmaWarp ? warp >> 2 : warp - kMmaWarp;   // the warp's stream
+    const uint32_t tm_s = tm + 128 * st, tm_o = tm + 256 + 128 * st;
+    auto q_uses = [&](int slot) { return slot ? q1_uses : q0_uses; };
+    auto use_q = [&](int slot) {
+      q0_uses += slot == 0;
+      q1_uses += slot == 1;
+    };
 
     if (warp == kTmaWarp) {
       // -------------------------------------------------------- loads -----
@@ -760,13 +788,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         y1_was = y1;
         int x = from + lane, i = 0;
         for (; i < n_items; ++i) {
-          const int nt = s.items[i].t1 - s.items[i].t0;
+          const Item& q = s.items[(first + i) % kMaxItems];
+          const int nt = q.t1 - q.t0;
           if (x < nt) break;
           x -= nt;
         }
         int id[2] = {p.n_pages, p.n_pages}, head = 0;    // beyond the pool: loads as zeros
         if (i < n_items) {
-          const Item& q = s.items[i];
+          const Item& q = s.items[(first + i) % kMaxItems];
           head = q.head;
           const int page = first_token(q, q.t0 + x) / kPageTokens;
 #pragma unroll
@@ -811,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item& q = w.at();
         for (int h = 0; h < (q.dual ? 2 : 1); ++h) {
           const int sl = w.q_slot(h);
-          if (qn[sl] > 0) ok = ok && wait(s, b_qempty + 8 * sl, (qn[sl] - 1) & 1, p);
+          if (q_uses(sl) > 0) ok = ok && wait(s, b_qempty + 8 * sl, (q_uses(sl) - 1) & 1, p);
           ok = __all_sync(kFull, ok);
           if (ok && lane == 0) {
             const bool one = q.nmem == 1;
@@ -824,10 +853,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                      q.b0 + h * p.MB, c2, b_qfull + 8 * sl);
           }
           __syncwarp();
-          qn[sl] += 1;
+          use_q(sl);
         }
       };
-      Walk k(s.items, n_items), v(s.items, n_items);
+      Walk k(s.items, n_items, first), v(s.items, n_items, first);
       int kt = 0, vt = 0;
       auto do_k = [&]() {
         if (k.first()) load_q(k);
@@ -840,149 +869,153 @@ __global__ void __launch_bounds__(kThreads, 1)
         v.next();
         if (ok && n + 2 < n_steps) do_k();
       }
-    } else if (warp == kMmaWarp) {
+    } else if (warp >= kMmaWarp) {
       // --------------------------------------------------------- MMAs -----
-      if (lane == 0) {
-        const uint32_t fmt = (1u << 4) | (Half<T>::kFormat << 7) | (Half<T>::kFormat << 10) |
-                             ((uint32_t)(kRows >> 4) << 24);
-        const uint32_t id_qk = fmt | ((uint32_t)(kTile >> 3) << 17);
-        const uint32_t id_pv = fmt | (1u << 16) | ((uint32_t)(HD >> 3) << 17);
-        Walk k(s.items, n_items), v(s.items, n_items);
-        uint32_t k_st = 0, v_st = 0;
-        int kstep = 0;
-        auto do_k = [&]() {
-          const int st = kstep & 1;
-          const int sl = k.q_slot(st);
-          if (k.loads()) {
-            k_st = ring % L::kStages;
-            ok = ok && wait(s, b_full + 8 * k_st, (ring / L::kStages) & 1, p);
-            ++ring;
-          }
-          if (k.first()) {
-            const int n = k.dual ? 2 : 1;
-            for (int h = 0; h < n; ++h) {
-              const int s2 = k.q_slot(h);
-              ok = ok && wait(s, b_qfull + 8 * s2, qn[s2] & 1, p);
-              qn[s2] += 1;
-            }
-          }
+      // Every lane keeps count, one issues.  Both warps pass over all tiles in the
+      // order of the ring; what a warp's stream does not use, it releases.
+      const uint32_t fmt = (1u << 4) | (Half<T>::kFormat << 7) | (Half<T>::kFormat << 10) |
+                           ((uint32_t)(kRows >> 4) << 24);
+      const uint32_t id_qk = fmt | ((uint32_t)(kTile >> 3) << 17);
+      const uint32_t id_pv = fmt | (1u << 16) | ((uint32_t)(HD >> 3) << 17);
+      Walk k(s.items, n_items, first), v(s.items, n_items, first);
+      uint32_t k_at = 0, v_at = 0;     // places in the ring
+      // a wait whose outcome is the same in every lane
+      auto hold = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(kFull, ok && wait(s, bar, parity, p)); };
+      auto hold_tile = [&](uint32_t at) { hold(b_full + 8 * (at % L::kStages), (at / L::kStages) & 1); };
+      auto release = [&](uint32_t bar) {
+        if (ok && lane == 0) mbar_arrive(bar);
+        __syncwarp();
+      };
+      auto do_k = [&](int n) {
+        if (k.loads()) k_at = ring++;
+        const uint32_t stage = k_at % L::kStages;
+        const int sl = k.q_slot(st);
+        if ((n & 1) == st) {
+          hold_tile(k_at);
+          if (k.first_of_stream()) hold(b_qfull + 8 * sl, q_uses(sl) & 1);
           if (!ok) return;
           tc_after();
           const uint32_t qa = sb + L::kQ + sl * L::kTileBytes;
-          const uint32_t ka = sb + L::kRing + k_st * L::kTileBytes;
+          const uint32_t ka = sb + L::kRing + stage * L::kTileBytes;
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kRows * 128 + (kk & 3) * 32;
-            mma_ss(tm_s[st], desc_of(qa + off, 16), desc_of(ka + off, 16), id_qk, kk > 0);
-          }
+          for (int c = 0; c < L::kChunks; ++c)
+            mma_ss4(tm_s, desc_of(qa + c * kRows * 128, 16), desc_of(ka + c * kTile * 128, 16), id_qk, c > 0);
           tc_commit(b_sfull + 8 * st);
-          if (k.frees()) tc_commit(b_empty + 8 * k_st);
-          // the run's last use of a slot
-          if (k.dual ? k.last_of_stream() : k.last()) tc_commit(b_qempty + 8 * sl);
-          k.next();
-          ++kstep;
-        };
-        for (int i = 0; i < 2 && i < n_steps && ok; ++i) do_k();
-        for (int n = 0; n < n_steps && ok; ++n) {
-          const int st = n & 1;
-          if (v.loads()) {
-            v_st = ring % L::kStages;
-            ok = ok && wait(s, b_full + 8 * v_st, (ring / L::kStages) & 1, p);
-            ++ring;
+          tc_commit(b_empty + 8 * stage);
+          if (k.last_of_stream()) tc_commit(b_qempty + 8 * sl);   // the run's last use of a slot
+        } else if (!k.dual) {
+          hold_tile(k_at);
+          release(b_empty + 8 * stage);
+        }
+        if (k.last()) {
+          // slots of the run that the stream has not used
+          if (k.dual || (k.total == 1 && (n & 1) != st)) {
+            const int other = k.dual ? st ^ 1 : sl;
+            hold(b_qfull + 8 * other, q_uses(other) & 1);
+            release(b_qempty + 8 * other);
           }
-          if (v.first_of_stream() && on[st] > 0) ok = ok && wait(s, b_ofree + 8 * st, (on[st] - 1) & 1, p);
-          const uint32_t va = sb + L::kRing + v_st * L::kTileBytes;
+          if (k.dual) {
+            use_q(0);
+            use_q(1);
+          } else {
+            use_q(sl);
+          }
+        }
+        k.next();
+      };
+      for (int i = 0; i < 2 && i < n_steps && ok; ++i) do_k(i);
+      for (int n = 0; n < n_steps && ok; ++n) {
+        if (v.loads()) v_at = ring++;
+        const uint32_t stage = v_at % L::kStages;
+        if ((n & 1) == st) {
+          hold_tile(v_at);
+          if (v.first_of_stream() && on > 0) hold(b_ofree + 8 * st, (on - 1) & 1);
+          const uint32_t va = sb + L::kRing + stage * L::kTileBytes;
           for (int half = 0; half < 2; ++half) {
-            ok = ok && wait(s, b_pready + 16 * st + 8 * half, sn[st] & 1, p);
+            hold(b_pready + 16 * st + 8 * half, sn & 1);
             if (!ok) break;
             tc_after();
-#pragma unroll
-            for (int k4 = 0; k4 < kTile / 32; ++k4) {
-              const int kk = half * (kTile / 32) + k4;
-              mma_ts(tm_o[st], tm_s[st] + kk * 8, desc_of(va + kk * 16 * 128, kTile * 128), id_pv,
-                     !(v.first_of_stream() && kk == 0));
-            }
+            mma_ts4(tm_o, tm_s + half * (kTile / 4),
+                    desc_of(va + half * (kTile / 2) * 128, kTile * 128), id_pv,
+                    !(v.first_of_stream() && half == 0));
           }
           if (!ok) break;
-          sn[st] += 1;
-          if (v.frees()) tc_commit(b_empty + 8 * v_st);
+          sn += 1;
+          tc_commit(b_empty + 8 * stage);
           if (v.last_of_stream()) {
             tc_commit(b_ofull + 8 * st);
-            on[st] += 1;
+            on += 1;
           }
-          v.next();
-          if (n + 2 < n_steps) do_k();
+        } else if (!v.dual) {
+          hold_tile(v_at);
+          release(b_empty + 8 * stage);
         }
+        v.next();
+        if (ok && n + 2 < n_steps) do_k(n + 2);
       }
-      ok = __all_sync(kFull, ok);
     } else {
       // ------------------------------------------------------ softmax -----
-      const int st = warp >> 2;                        // stream
+      // A wait that runs out ends no loop here: once one has, all return at once.
       const int r = threadIdx.x & (kGroupThreads - 1); // row
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 lanes
-      const uint32_t ts = tm_s[st] + lanes;
-      Walk w(s.items, n_items);
-      uint32_t kloads = 0, vloads = 0;                 // among the steps so far
-      float m = -INFINITY, l = 0.0f;
+      const uint32_t ts = tm_s + lanes;
+      const uint32_t bar_s = b_sfull + 8 * st, bar_p = b_pready + 16 * st;
       const int j = r / p.G;                           // entry among the rows, less b0
-      bool busy = false, shared = false;               // rows of this warp meet the item; have to be 0
-      int slot = -2, lim = 0;                          // the row's partial result; -2: none
-      for (int n = 0; n < n_steps && ok; ++n) {
-        const Item& q = w.at();
-        if (w.loads()) {
-          ++kloads;
-          ++vloads;
-        }
-        if (w.first()) {
+      float m = -INFINITY, l = 0.0f;
+      int slot = -2;                                   // the row's partial result; -2: none
+      int n0 = 0, tiles = 0;                           // steps and tiles of the items before
+      for (int i = 0; i < n_items; ++i) {
+        const Item& q = s.items[(first + i) % kMaxItems];
+        const bool dual = q.dual, own = q.own;
+        const int nt = q.t1 - q.t0, steps = dual ? 2 * nt : nt;
+        const int lo = q.lo, hi = q.hi;
+        const int a0 = first_token(q, q.t0);
+        if (q.j0 == 0) {
           m = -INFINITY;
           l = 0.0f;
           slot = -2;
         }
-        if (w.enters()) {
-          // this thread's row of the item
-          const int e = (w.dual ? st * p.MB : 0) + j;
-          const bool real = j < p.MB && (q.own ? q.b0 + e == q.row : e < q.nmem);
-          shared = q.own;
-          busy = __any_sync(kFull, real);
-          lim = 0;
-          if (real) {
-            slot = q.slot;
-            lim = q.hi;
-            if (!q.own) {
-              const int pos = __ldg(p.positions + q.b0 + e);
-              lim = min(pos < 0 || pos >= p.max_pages * kPageTokens ? 0 : pos + 1, q.hi);
-            }
+        // this thread's row of the item
+        const int e = (dual ? st * p.MB : 0) + j;
+        const bool real = j < p.MB && (own ? q.b0 + e == q.row : e < q.nmem);
+        const bool busy = __any_sync(kFull, real);
+        int lim = 0;                                   // tokens that the row sees
+        if (real) {
+          slot = q.slot;
+          lim = hi;
+          if (!own) {
+            const int pos = __ldg(p.positions + q.b0 + e);
+            lim = min(pos < 0 || pos >= p.max_pages * kPageTokens ? 0 : pos + 1, hi);
           }
         }
-        if ((n & 1) == st) {
-          const int a = first_token(q, w.tile());
-          ok = ok && wait(s, b_sfull + 8 * st, sn[st] & 1, p);
-          if (!__all_sync(kFull, ok)) {
-            ok = false;
-            break;
-          }
-          sn[st] += 1;
+        const int all_see = __reduce_min_sync(kFull, lim);
+        for (int u = (st ^ n0) & 1; u < steps; u += 2) {
+          const int tile = dual ? u >> 1 : u;
+          const int a = a0 + tile * kTile;             // the tile's first token
+          const bool masked = a < lo || a + kTile > all_see;
+          wait(s, bar_s, sn & 1, p);
+          sn += 1;
+          __syncwarp();
+          // the row's scores, 32 at a time and the next 32 on their way: read twice,
+          // since registers for all of them would leave too few for the rest
           uint32_t x[32], y[32];
-          float f_old = 1.0f, ref = 0.0f;
-          const bool masked = __any_sync(kFull, a < q.lo || a + kTile > lim);
-          // scores of tokens that are not the row's, in columns c .. c + 31
-          auto mask = [&](uint32_t* v, int c) {
+          auto mask = [&](uint32_t* v, int c) {        // tokens that are not the row's
             if (!masked) return;
-            const int lo = q.lo - a - c, hi = lim - a - c;
-            const uint32_t below = lo <= 0 ? 0u : lo >= 32 ? kFull : (1u << lo) - 1u;
-            const uint32_t keep = (hi <= 0 ? 0u : hi >= 32 ? kFull : (1u << hi) - 1u) & ~below;
+            auto bits = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
+            const uint32_t keep = bits(lim - a - c) & ~bits(lo - a - c);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((keep >> i) & 1u)) v[i] = 0xff800000u;
+            for (int k = 0; k < 32; ++k)
+              if (!((keep >> k) & 1u)) v[k] = 0xff800000u;
           };
+          float ref = 0.0f;
           if (busy) {
             tc_after();
             float t0 = -INFINITY, t1 = -INFINITY;
             auto largest = [&](const uint32_t* v) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                t0 = max3(t0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                t1 = max3(t1, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+              for (int k = 0; k < 32; k += 4) {
+                t0 = max3(t0, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                t1 = max3(t1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
               }
             };
             tmem_ld32(ts, x);
@@ -1002,81 +1035,87 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a score that is no number, or +infinity, makes the sum NaN
             if (top != -INFINITY) l += top - top;
             const bool grow = top > m + kRescale;      // also the first score of a row
-            const float m_old = m;
+            const bool some = grow && m != -INFINITY;
+            float f_old = 1.0f;
             if (grow) {
               f_old = ex2(m - top);                    // 0 for the first
               l *= f_old;
               m = top;
             }
             // O of a row without a score so far is 0 already
-            if (__any_sync(kFull, grow && m_old != -INFINITY)) {
+            if (__any_sync(kFull, some)) {
               // S of this step was committed after P V of the stream's last
               // one, so O is at rest
-              const uint32_t to = tm_o[st] + lanes;
 #pragma unroll 1
-              for (int i = 0; i < HD; i += 32) {
-                tmem_ld32(to + i, y);
+              for (int c = 0; c < HD; c += 32) {
+                tmem_ld32(tm_o + lanes + c, y);
                 tmem_wait_ld32(y);
 #pragma unroll
-                for (int k2 = 0; k2 < 32; ++k2) y[k2] = __float_as_uint(__uint_as_float(y[k2]) * f_old);
-                tmem_st32(to + i, y);
+                for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f_old);
+                tmem_st32(tm_o + lanes + c, y);
               }
             }
             ref = (m == -INFINITY ? 0.0f : m) - Half<T>::kShift;
           }
-          if (ragged(q, a)) {
-            // clear V's rows of tokens that are not the unit's.  The tile's
-            // place in the ring: behind the V tiles so far and the K tiles of
-            // the steps up to the one after that which loaded it.
-            Walk nx = w;
-            nx.next();
-            const uint32_t ahead = w.loads() && !nx.done() && nx.loads() ? 1 : 0;
-            const uint32_t at = ring + kloads + ahead + vloads - 1;
+          if (a < lo || (a + kTile > hi && hi % kPageTokens)) {
+            // Clear V's rows of tokens inside the loaded pages that are not the
+            // unit's: what lies there is not the sequence's, and 0 x infinity would
+            // spoil the row.  The tile's place in the ring is behind the V tiles
+            // before and the K tiles of the steps up to the one after that which
+            // loaded it.
+            const uint32_t at = ring + 2 * (tiles + tile) + 1 + (!dual && n0 + u + 1 < n_steps ? 1 : 0);
             const uint32_t vs = at % L::kStages;
-            ok = wait(s, b_full + 8 * vs, (at / L::kStages) & 1, p);
-            if (ok) {
+            if (wait(s, b_full + 8 * vs, (at / L::kStages) & 1, p)) {
               const uint32_t va = sb + L::kRing + vs * L::kTileBytes;
               auto clear = [&](int tok0, int tok1) {
-                for (int i = tok0 * 8 + r; i < tok1 * 8; i += kGroupThreads)
+                for (int k = tok0 * 8 + r; k < tok1 * 8; k += kGroupThreads)
 #pragma unroll
-                  for (int c2 = 0; c2 < L::kChunks; ++c2)
+                  for (int c = 0; c < L::kChunks; ++c)
                     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                     va + c2 * kTile * 128 + i * 16),
+                                     va + c * kTile * 128 + k * 16),
                                  "r"(0)
                                  : "memory");
               };
-              clear(0, min(max(q.lo - a, 0), kTile));
-              if (a + kTile > q.hi) {
-                const int end = max(q.hi - a, 0);
-                clear(end, min(kTile, (end + kPageTokens - 1) / kPageTokens * kPageTokens));
-              }
+              if (a < lo) clear(0, min(lo - a, kTile));
+              if (a + kTile > hi)
+                clear(max(hi - a, 0), min(kTile, (max(hi - a, 0) + kPageTokens - 1) / kPageTokens * kPageTokens));
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
-            if (!__all_sync(kFull, ok)) {
-              ok = false;
-              break;
-            }
+            __syncwarp();
           }
+          // The streams take their exponentials in turn: in phase, both would
+          // wait for the special-function units first and for the MMAs then.
+          // Only the pace depends on it.
+          auto my_turn = [&]() {
+            const uint32_t before = turns + (uint32_t)(n0 + u + st) / 2;   // steps of the other stream so far
+            if (before > 0) wait(s, b_turn + 8 * st, (before - 1) & 1, p);
+            __syncwarp();
+          };
+          auto pass_turn = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_turn + 8 * (st ^ 1));
+          };
           if (busy) {
+            my_turn();
             const uint64_t c2 = pair(p.c, p.c), r2 = pair(-ref, -ref);
             uint64_t sum[2] = {0, 0};
             auto weigh = [&](const uint32_t* v, int c) {
               uint32_t o[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                uint64_t e = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), c2, r2);
-                float ea, eb;
-                if (i * kFmaPairs / 16 != (i + 1) * kFmaPairs / 16) {
-                  e = exp2_pair(e);
-                  unpair(e, ea, eb);
+              for (int k = 0; k < 16; ++k) {
+                uint64_t w = fma2(pair(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, r2);
+                float wa, wb;
+                if (k * kFmaPairs / 16 != (k + 1) * kFmaPairs / 16) {
+                  w = exp2_pair(w);
+                  unpair(w, wa, wb);
                 } else {
-                  unpair(e, ea, eb);
-                  ea = ex2(ea);
-                  eb = ex2(eb);
-                  e = pair(ea, eb);
+                  unpair(w, wa, wb);
+                  wa = ex2(wa);
+                  wb = ex2(wb);
+                  w = pair(wa, wb);
                 }
-                sum[i & 1] = add2(sum[i & 1], e);
-                o[i] = Half<T>::pack(ea, eb);
+                sum[k & 1] = add2(sum[k & 1], w);
+                o[k] = Half<T>::pack(wa, wb);
               }
               tmem_st16(ts + c / 2, o);        // over columns whose scores have been read
             };
@@ -1084,50 +1123,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kTile; c += 64) {
               tmem_ld32(ts + c + 32, y);
               mask(x, c);
-              tmem_wait_ld32(y);
               weigh(x, c);
+              tmem_wait_ld32(y);
               if (c == 0) tmem_ld32(ts + 64, x);
               mask(y, c + 32);
               weigh(y, c + 32);
               if (c == 0) tmem_wait_ld32(x);
+              else pass_turn();
               tmem_wait_st();
               tc_before();
-              mbar_arrive(b_pready + 16 * st + (c ? 8 : 0));
+              mbar_arrive(bar_p + (c ? 8 : 0));
             }
             float s0, s1, s2, s3;
             unpair(sum[0], s0, s1);
             unpair(sum[1], s2, s3);
             l += (s0 + s1) + (s2 + s3);
           } else {
-            if (shared) {              // other entries' tokens: no weight
+            if (own) {                 // other entries' tokens: no weight
               tc_after();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = 0;
+              for (int k = 0; k < 32; ++k) x[k] = 0;
               tmem_st32(ts, x);
               tmem_st32(ts + 32, x);
               tmem_wait_st();
               tc_before();
             }
-            mbar_arrive(b_pready + 16 * st);
-            mbar_arrive(b_pready + 16 * st + 8);
+            pass_turn();
+            mbar_arrive(bar_p);
+            mbar_arrive(bar_p + 8);
           }
         }
-        if (w.last()) {
+        n0 += steps;
+        tiles += nt;
+        if (q.j0 + steps == q.steps) {
           // ----------------------------------------------- the run's end --
-          const bool took = w.total >= 2 || (n & 1) == st;   // this stream took part
+          const int last = (n0 - 1) & 1;                     // stream of its last step
+          const bool took = q.steps >= 2 || last == st;      // this stream took part
           if (took) {
-            ok = wait(s, b_ofull + 8 * st, on[st] & 1, p);
-            if (!__all_sync(kFull, ok)) {
-              ok = false;
-              break;
-            }
+            wait(s, b_ofull + 8 * st, on & 1, p);
+            on += 1;
+            __syncwarp();
           }
           if (__any_sync(kFull, slot != -2)) {
             float* dst = nullptr;
             if (slot != -2) {
-              const int b = q.b0 + (w.dual ? st * p.MB : 0) + j, hq = q.head * p.G + r % p.G;
+              const int hq = q.head * p.G + r % p.G;
               const size_t row = slot >= 0 ? ((size_t)slot * 2 + st) * kRows + r
-                                           : whole_row(p, q.own ? 1 : 0, w.dual ? 0 : st, b, hq);
+                                           : whole_row(p, own ? 1 : 0, dual ? 0 : st, q.b0 + e, hq);
               dst = p.part + row * HD;
               // without a step of its own the stream has seen nothing, and O is not its
               p.part_ml[row] = make_float2((m == -INFINITY ? 0.0f : m) - Half<T>::kShift, took ? l : 0.0f);
@@ -1135,29 +1177,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (took) {
               tc_after();
 #pragma unroll 1
-              for (int i = 0; i < HD; i += 32) {
+              for (int c = 0; c < HD; c += 32) {
                 uint32_t o[32];
-                tmem_ld32(tm_o[st] + lanes + i, o);
+                tmem_ld32(tm_o + lanes + c, o);
                 tmem_wait_ld32(o);
                 if (slot != -2) {
 #pragma unroll
-                  for (int k2 = 0; k2 < 32; k2 += 4)
-                    *reinterpret_cast<uint4*>(dst + i + k2) =
-                        make_uint4(o[k2], o[k2 + 1], o[k2 + 2], o[k2 + 3]);
+                  for (int k = 0; k < 32; k += 4)
+                    *reinterpret_cast<uint4*>(dst + c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                 }
               }
               tc_before();
             }
           }
           if (took) mbar_arrive(b_ofree + 8 * st);
-          // both groups keep both streams' counts
-          for (int t = 0; t < 2; ++t)
-            if (w.total >= 2 || (n & 1) == t) on[t] += 1;
         }
-        w.next();
       }
-      // the other roles' ring count
-      ring += kloads + vloads;
+      ring += 2 * tiles;               // the other roles' ring count
+      turns += (uint32_t)(n_steps + st) / 2;
     }
     __syncthreads();
     ok = ok && *(volatile int*)&s.abort == 0;
@@ -1363,9 +1400,10 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ptr,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kMaxDevices = 64;
+
 // Streaming multiprocessors of a device (looked up once per device).
 int sm_count(int device) {
-  constexpr int kMaxDevices = 64;
   static std::once_flag once[kMaxDevices];
   static int count[kMaxDevices];
   if (device < 0 || device >= kMaxDevices) return 0;
@@ -1422,14 +1460,24 @@ cudaError_t launch(void (*kernel)(P...), unsigned blocks, unsigned threads, size
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The kernel's right to its shared memory, asked for once per device.
 template <typename T, int HD>
-cudaError_t launch_attention(const AttnParams& p, const CUtensorMap* maps, cudaStream_t st) {
-  using L = Layout<HD>;
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<T, HD>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDyn);
+cudaError_t allow_shared(int device) {
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t result[kMaxDevices];
+  std::call_once(once[device], [&] {
+    result[device] = cudaFuncSetAttribute(attention_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          Layout<HD>::kDyn);
+  });
+  return result[device];
+}
+
+template <typename T, int HD>
+cudaError_t launch_attention(const AttnParams& p, const CUtensorMap* maps, int device, cudaStream_t st) {
+  cudaError_t e = allow_shared<T, HD>(device);
   if (e != cudaSuccess) return e;
-  e = launch(attention_kernel<T, HD>, (unsigned)p.grid, kThreads, L::kDyn, st, p, maps[0], maps[1], maps[2],
-             maps[3]);
+  e = launch(attention_kernel<T, HD>, (unsigned)p.grid, kThreads, Layout<HD>::kDyn, st, p, maps[0], maps[1],
+             maps[2], maps[3]);
   if (e != cudaSuccess) return e;
   const unsigned rows = (unsigned)(p.B * p.Hq);
   if (rows <= kWideJoin) return launch(join_kernel<T, HD, 4>, rows, 128, 0, st, p);
@@ -1524,10 +1572,10 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* a, void
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a->type == MK_BF16)
-    e = a->head_dim == 128 ? launch_attention<__nv_bfloat16, 128>(p, maps, st)
-                           : launch_attention<__nv_bfloat16, 64>(p, maps, st);
+    e = a->head_dim == 128 ? launch_attention<__nv_bfloat16, 128>(p, maps, a->device, st)
+                           : launch_attention<__nv_bfloat16, 64>(p, maps, a->device, st);
   else
-    e = a->head_dim == 128 ? launch_attention<__half, 128>(p, maps, st)
-                           : launch_attention<__half, 64>(p, maps, st);
+    e = a->head_dim == 128 ? launch_attention<__half, 128>(p, maps, a->device, st)
+                           : launch_attention<__half, 64>(p, maps, a->device, st);
   return from_cuda(e);
 }

@@ -117,10 +117,11 @@ def _load():
         "mk_debug_size": (c_size_t, [c_void_p, c_int]),
         "mk_plan_schedule": (c_int, [P(mk_config), c_int, c_int, P(c_int32), P(c_int32),
                                      P(c_int32), P(c_int32), P(c_int32)]),
-        "mk_rope_append": (c_int, [P(mk_rope_append_args), c_void_p]),
-        "mk_prefix_attention_workspace": (c_size_t, [P(mk_prefix_attention_args)]),
-        "mk_prefix_attention": (c_int, [P(mk_prefix_attention_args), c_void_p]),
-        "mk_sample": (c_int, [P(mk_sample_args), c_void_p]),
+        # an argument struct by reference, or its bytes
+        "mk_rope_append": (c_int, [c_void_p, c_void_p]),
+        "mk_prefix_attention_workspace": (c_size_t, [c_void_p]),
+        "mk_prefix_attention": (c_int, [c_void_p, c_void_p]),
+        "mk_sample": (c_int, [c_void_p, c_void_p]),
         "mk_strerror": (c_char_p, [c_int]),
         "mk_destroy": (None, [c_void_p]),
     }

@@ -12,9 +12,8 @@ streams may overlap it as long as they write other tensors.
 
 from __future__ import annotations
 
-import ctypes
 import math
-from ctypes import byref, c_void_p
+import struct
 from typing import Optional
 
 import torch
@@ -24,7 +23,8 @@ from . import mk
 PAGE = 64
 
 _TYPE = {torch.float32: mk.MK_FP32, torch.bfloat16: mk.MK_BF16, torch.float16: mk.MK_FP16}
-_I32 = torch.int32
+_POOL = (torch.bfloat16, torch.float16)
+_I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
 _OPS = {mk.MK_OP_ROPE_APPEND: "rope_append", mk.MK_OP_PREFIX_ATTENTION: "prefix_attention",
         mk.MK_OP_SAMPLE: "sample"}
 
@@ -49,53 +49,59 @@ class Status:
             raise mk.MKError(rc, _OPS.get(detail[0], "device status"), detail)
 
 
-def _index(t: torch.Tensor, name: str, dev, shape) -> int:
-    if t.dtype != _I32 or t.device != dev:
-        raise TypeError(f"{name} must be an int32 tensor on {dev}")
+# The calls below are as short as a decode step's, and so are their checks:
+# devices are compared by number, and the arguments are packed in one go in the
+# layout of the C structs (fields as in mk.mk_*_args).
+_PACK_APPEND = struct.Struct("@12if3P6q8P").pack
+_PACK_ATTENTION = struct.Struct("@9ifPq9PNP").pack
+_PACK_SAMPLE = struct.Struct("@4iPq8P").pack
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _array(t: torch.Tensor, dtype, name: str, dev: int, shape) -> int:
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be a {str(dtype)[6:]} tensor on cuda:{dev}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
     return t.data_ptr()
 
 
-def _float(t: torch.Tensor, name: str, dev, shape) -> int:
-    if t.dtype != torch.float32 or t.device != dev:
-        raise TypeError(f"{name} must be a float32 tensor on {dev}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
-    return t.data_ptr()
-
-
-def _cuda(t: torch.Tensor, name: str):
-    if not t.is_cuda:
+def _cuda(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return t.device
+    return dev
 
 
-def _stream(stream, dev) -> c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    return c_void_p(s.cuda_stream)
+def _stream(stream, dev: int) -> int:
+    """The stream's handle.  Without one, the current stream of the device."""
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream must be of cuda:{dev}")
+    return stream.cuda_stream
 
 
-def _status(status: Optional[Status], dev):
+def _status(status: Optional[Status], dev: int) -> int:
     if status is None:
-        return None
-    if status.word.device != dev:
-        raise ValueError(f"status must be on {dev}")
+        return 0
+    if status.word.get_device() != dev:
+        raise ValueError(f"status must be on cuda:{dev}")
     return status.word.data_ptr()
 
 
-def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor, dev):
-    """Checks one layer's pools; returns their shape (pages, heads, head size)."""
-    if k_pool.dtype not in (torch.bfloat16, torch.float16) or v_pool.dtype != k_pool.dtype:
+def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor, dev: int):
+    """Checks one layer's pools; returns their type and shape (pages, heads, head size)."""
+    dtype, shape = k_pool.dtype, k_pool.shape
+    if dtype not in _POOL or v_pool.dtype is not dtype:
         raise TypeError("k_pool and v_pool must both be bfloat16 or both float16")
-    if k_pool.device != dev or v_pool.device != dev:
-        raise TypeError(f"k_pool and v_pool must be on {dev}")
-    shape = k_pool.shape
+    if k_pool.get_device() != dev or v_pool.get_device() != dev:
+        raise TypeError(f"k_pool and v_pool must be on cuda:{dev}")
     if len(shape) != 4 or v_pool.shape != shape or shape[2] != PAGE or shape[3] not in (64, 128):
         raise ValueError("k_pool and v_pool must be [pages][kv heads][64][64 or 128]")
     if not k_pool.is_contiguous() or not v_pool.is_contiguous():
         raise ValueError("k_pool and v_pool must be contiguous")
-    return shape[0], shape[1], shape[3]
+    return dtype, shape[0], shape[1], shape[3]
 
 
 def rope_frequencies(rotary_dim: int, theta: float = 1.0e4, *, scaling: Optional[str] = None,
@@ -153,53 +159,56 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     ``rope_frequencies``.  Returns q_out ([tokens][query heads][hd] of the
     pools' type; allocated if None, may be q itself), None without queries."""
     dev = _cuda(k, "k")
-    n_pages, hkv, hd = _pools(k_pool, v_pool, dev)
-    t = k.shape[0]
-    src = _TYPE.get(k.dtype)
-    if src is None or v.dtype != k.dtype or v.device != dev:
+    pool, n_pages, hkv, hd = _pools(k_pool, v_pool, dev)
+    dtype, shape = k.dtype, k.shape
+    t = shape[0]
+    if dtype not in _TYPE or v.dtype is not dtype or v.get_device() != dev:
         raise TypeError("k and v must have the same type (float32, bfloat16 or float16) and device")
-    if k.shape != (t, hkv, hd) or v.shape != k.shape:
+    if shape != (t, hkv, hd) or v.shape != shape:
         raise ValueError(f"k and v must be [tokens][{hkv}][{hd}]")
     ks, vs = k.stride(), v.stride()
     if t and (ks[2] != 1 or vs[2] != 1):
         raise ValueError("the columns of k and v must be adjacent")
-    hq, qs = 0, (0, 0, 1)
+    hq, qs, q_at, out_at = 0, (0, 0, 1), 0, 0
     if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        if q.shape != (t, hq, hd) or hq < 1:
+        shape = q.shape
+        hq = shape[1] if len(shape) == 3 else 0
+        if shape != (t, hq, hd) or hq < 1:
             raise ValueError(f"q must be [tokens][query heads][{hd}]")
-        if q.dtype != k.dtype or q.device != dev:
+        if q.dtype is not dtype or q.get_device() != dev:
             raise TypeError("q must have the type and device of k")
         qs = q.stride()
         if t and qs[2] != 1:
             raise ValueError("the columns of q must be adjacent")
         if q_out is None:
-            q_out = torch.empty((t, hq, hd), dtype=k_pool.dtype, device=dev)
-        elif (q_out.shape != (t, hq, hd) or not q_out.is_contiguous()
-              or q_out.dtype != k_pool.dtype or q_out.device != dev):
+            q_out = torch.empty((t, hq, hd), dtype=pool, device=q.device)
+        elif (q_out.shape != shape or not q_out.is_contiguous() or q_out.dtype is not pool
+              or q_out.get_device() != dev):
             raise ValueError("q_out must be contiguous, shaped like q and of the pools' type and device")
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if inv_freq.dtype != torch.float64 or inv_freq.device != dev or not inv_freq.is_contiguous():
-        raise TypeError(f"inv_freq must be a contiguous float64 tensor on {dev}")
-    if inv_freq.dim() != 1 or 2 * inv_freq.numel() > hd:
+    if inv_freq.dtype is not _F64 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
+        raise TypeError(f"inv_freq must be a contiguous float64 tensor on cuda:{dev}")
+    freqs = inv_freq.numel()
+    if inv_freq.dim() != 1 or 2 * freqs > hd:
         raise ValueError(f"inv_freq must hold at most {hd // 2} frequencies")
-    if page_table.dim() != 2:
+    table = page_table.shape
+    if len(table) != 2:
         raise ValueError("page_table must be [rows][pages per row]")
-    rows = page_table.shape[0]
-    if seq is None and t > rows:
+    if seq is None and t > table[0]:
         raise ValueError("more tokens than page-table rows, and no seq")
-    a = mk.mk_rope_append_args(
-        dev.index, t, rows, page_table.shape[1], n_pages, hq, hkv, hd, 2 * inv_freq.numel(),
-        1 if interleaved else 0, src, _TYPE[k_pool.dtype], magnitude,
-        q.data_ptr() if q is not None else None, k.data_ptr(), v.data_ptr(),
-        qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
-        q_out.data_ptr() if q is not None else None, k_pool.data_ptr(), v_pool.data_ptr(),
-        inv_freq.data_ptr(), _index(positions, "positions", dev, (t,)),
-        _index(seq, "seq", dev, (t,)) if seq is not None else None,
-        _index(page_table, "page_table", dev, page_table.shape), _status(status, dev))
+    a = _PACK_APPEND(
+        dev, t, table[0], table[1], n_pages, hq, hkv, hd, 2 * freqs, 1 if interleaved else 0, _TYPE[dtype],
+        _TYPE[pool], magnitude, q_at, k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+        out_at, k_pool.data_ptr(), v_pool.data_ptr(), inv_freq.data_ptr(),
+        _array(positions, _I32, "positions", dev, (t,)), 0 if seq is None else _array(seq, _I32, "seq", dev, (t,)),
+        _array(page_table, _I32, "page_table", dev, table), _status(status, dev))
+    handle = _stream(stream, dev)
     if t:
-        mk.check_status(mk.lib.mk_rope_append(byref(a), _stream(stream, dev)), "mk_rope_append")
+        rc = mk.lib.mk_rope_append(a, handle)
+        if rc:
+            raise mk.MKError(rc, "mk_rope_append")
     return q_out
 
 
@@ -223,47 +232,47 @@ def prefix_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
     are then zero); lse, if given, float32[batch][query heads], receives the log
     of each row's sum of exponentials."""
     dev = _cuda(q, "q")
-    n_pages, hkv, hd = _pools(k_pool, v_pool, dev)
-    if q.dim() != 3 or q.shape[2] != hd:
+    dtype, n_pages, hkv, hd = _pools(k_pool, v_pool, dev)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != hd:
         raise ValueError(f"q must be [batch][query heads][{hd}]")
-    b, hq, _ = q.shape
-    if q.dtype != k_pool.dtype:
+    b, hq, _ = shape
+    if q.dtype is not dtype:
         raise TypeError("q must have the pools' type")
     qs = q.stride()
     if b and (qs[2] != 1 or qs[1] != hd or qs[0] % 8):
         raise ValueError("q's heads must be adjacent and its token stride a multiple of 8")
     if hq < 1 or hq % hkv:
         raise ValueError("query heads must be a multiple of the kv heads")
-    if page_table.dim() != 2 or group_start.dim() != 1 or prefix_lens.dim() != 1:
+    if page_table.dim() != 2 or prefix_lens.dim() != 1:
         raise ValueError("page_table must be [batch][pages per row], group_start and prefix_lens flat")
-    n = prefix_lens.shape[0]
+    n, pages = prefix_lens.shape[0], page_table.shape[1]
     if out is None:
-        out = torch.zeros((b, hq, hd), dtype=q.dtype, device=dev)
-    elif (out.shape != (b, hq, hd) or not out.is_contiguous() or out.dtype != q.dtype
-          or out.device != dev):
+        out = torch.zeros(shape, dtype=dtype, device=q.device)
+    elif (out.shape != shape or not out.is_contiguous() or out.dtype is not dtype
+          or out.get_device() != dev):
         raise ValueError("out must be contiguous with q's shape, type and device")
-    a = mk.mk_prefix_attention_args(
-        dev.index, b, n, page_table.shape[1], n_pages, hq, hkv, hd, _TYPE[q.dtype],
-        scale if scale is not None else 1.0 / math.sqrt(hd), q.data_ptr(), qs[0],
-        k_pool.data_ptr(), v_pool.data_ptr(),
-        _index(page_table, "page_table", dev, (b, page_table.shape[1])),
-        _index(positions, "positions", dev, (b,)),
-        _index(group_start, "group_start", dev, (n + 1,)),
-        _index(prefix_lens, "prefix_lens", dev, (n,)), out.data_ptr(),
-        _float(lse, "lse", dev, (b, hq)) if lse is not None else None, None, 0,
-        _status(status, dev))
+    handle = _stream(stream, dev)
+    args = (dev, b, n, pages, n_pages, hq, hkv, hd, _TYPE[dtype],
+            1.0 / math.sqrt(hd) if scale is None else scale, q.data_ptr(), qs[0], k_pool.data_ptr(),
+            v_pool.data_ptr(), _array(page_table, _I32, "page_table", dev, (b, pages)),
+            _array(positions, _I32, "positions", dev, (b,)),
+            _array(group_start, _I32, "group_start", dev, (n + 1,)),
+            _array(prefix_lens, _I32, "prefix_lens", dev, (n,)), out.data_ptr(),
+            0 if lse is None else _array(lse, _F32, "lse", dev, (b, hq)))
+    st = _status(status, dev)
     if b == 0 or n == 0:
         return out
-    size = mk.lib.mk_prefix_attention_workspace(byref(a))
+    size = mk.lib.mk_prefix_attention_workspace(_PACK_ATTENTION(*args, 0, 0, st))
     # the workspace is this call's own; torch hands its memory on in stream order
     if stream is None:
-        work = torch.empty(size, dtype=torch.uint8, device=dev)
+        work = torch.empty(size, dtype=torch.uint8, device=q.device)
     else:
         with torch.cuda.stream(stream):
-            work = torch.empty(size, dtype=torch.uint8, device=dev)
-    a.workspace, a.workspace_bytes = work.data_ptr(), size
-    mk.check_status(mk.lib.mk_prefix_attention(byref(a), _stream(stream, dev)),
-                    "mk_prefix_attention")
+            work = torch.empty(size, dtype=torch.uint8, device=q.device)
+    rc = mk.lib.mk_prefix_attention(_PACK_ATTENTION(*args, work.data_ptr(), size, st), handle)
+    if rc:
+        raise mk.MKError(rc, "mk_prefix_attention")
     return out
 
 
@@ -288,24 +297,27 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch
     kind = _TYPE.get(logits.dtype)
     if kind is None:
         raise TypeError("logits must be float32, bfloat16 or float16")
-    if logits.dim() != 2 or logits.shape[1] < 1:
+    shape = logits.shape
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError("logits must be [batch][vocab]")
-    b, v = logits.shape
+    b, v = shape
     ls = logits.stride()
     if b and ls[1] != 1 and v > 1:
         raise ValueError("the columns of logits must be adjacent")
     rows = (b,)
     if tokens is None:
-        tokens = torch.empty(b, dtype=_I32, device=dev)
-    a = mk.mk_sample_args(
-        dev.index, b, v, kind, logits.data_ptr(), ls[0], _float(u, "u", dev, rows),
-        _float(temperature, "temperature", dev, rows) if temperature is not None else None,
-        _index(top_k, "top_k", dev, rows) if top_k is not None else None,
-        _float(top_p, "top_p", dev, rows) if top_p is not None else None,
-        _float(min_p, "min_p", dev, rows) if min_p is not None else None,
-        _index(tokens, "tokens", dev, rows),
-        _float(logprobs, "logprobs", dev, rows) if logprobs is not None else None,
-        _status(status, dev))
+        tokens = torch.empty(b, dtype=_I32, device=logits.device)
+    a = _PACK_SAMPLE(
+        dev, b, v, kind, logits.data_ptr(), ls[0], _array(u, _F32, "u", dev, rows),
+        0 if temperature is None else _array(temperature, _F32, "temperature", dev, rows),
+        0 if top_k is None else _array(top_k, _I32, "top_k", dev, rows),
+        0 if top_p is None else _array(top_p, _F32, "top_p", dev, rows),
+        0 if min_p is None else _array(min_p, _F32, "min_p", dev, rows),
+        _array(tokens, _I32, "tokens", dev, rows),
+        0 if logprobs is None else _array(logprobs, _F32, "logprobs", dev, rows), _status(status, dev))
+    handle = _stream(stream, dev)
     if b:
-        mk.check_status(mk.lib.mk_sample(byref(a), _stream(stream, dev)), "mk_sample")
+        rc = mk.lib.mk_sample(a, handle)
+        if rc:
+            raise mk.MKError(rc, "mk_sample")
     return tokens
