@@ -15,12 +15,13 @@
 // rows against its own tokens; the entries of a chunk (MB consecutive ones)
 // share one tile of query rows, and one after another meet their tokens with
 // the other entries' rows masked, so that a block works through many short
-// remainders without a break.  The tiles of all units form one line, measured
-// in steps (one 128 x 128 S tile; a prefix tile that serves two tiles of rows
-// is two); every block takes an equal stretch of it.  Each block finds its
-// stretch from the device arrays: the host needs no lengths, and a captured
-// graph replays with new ones.  A block's share of a unit leaves partial
-// results (O, m, l); a second launch adds them up.
+// remainders without a break.  The tiles of all units form one line, and every
+// block takes an equal stretch of it, so a long prefix is split over many blocks.
+// (A tile costs about the same whatever its rows: of 256 entries on 32768 tokens,
+// 5300 cycles with two tiles of rows and 5000 with one entry's.)  Each block finds
+// its stretch from the device arrays: the host needs no lengths, and a captured
+// graph replays with new ones.  A block's share of a unit leaves partial results
+// (O, m, l); a second launch adds them up.
 //
 // One block: a TMA warp streams K and V tiles, two warps issue tcgen05 MMAs,
 // and two groups of four warps hold a softmax row per thread.  S = Q K^T and O
@@ -63,13 +64,14 @@ constexpr int kWaitCycles = 1 << 30; // about half a second at any clock
 // in the line of its unit's first prefix tile and of its first own tile for KV
 // head 0, how far the next head's are, and how many tiles there are.
 struct __align__(16) Entry {
-  int prefix_at, prefix_tiles, prefix_width;   // steps a tile
+  int prefix_at, prefix_tiles;
+  int dual;                          // two tiles of rows meet each prefix tile
   int own_at, own_tiles, own_stride;
   int lead;                          // first entry of its prefix unit; -1: the entry is in no group
   int group;
 };
 struct Line {                        // the line of tiles and how blocks share it
-  int total, blocks, each, extra;    // block i has `each` steps, the first `extra` blocks one more
+  int total, blocks, each, extra;    // block i has `each` tiles, the first `extra` blocks one more
   __device__ __forceinline__ Line(int all, int grid) {
     total = all;
     blocks = max(1, min(grid, all));
@@ -429,7 +431,7 @@ __device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip,
   int32_t* seen = pl + n + 1;                      // [B]
   int32_t* group = seen + B;                       // [B]; -1: none
   int32_t* most = group + B;                       // [B]: prefix tokens that a leader's unit sees
-  int32_t* ppre = most + B;                        // [B]: steps of the prefix units led below
+  int32_t* ppre = most + B;                        // [B]: tiles of the prefix units led below
   int32_t* pre = ppre + B;                         // [B + 1]: own tiles of lower entries
   int32_t* cnt = pre + B + 1;                      // [B + 1]: lower entries that have any
   const int limit = p.max_pages * kPageTokens;
@@ -480,32 +482,29 @@ __device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip,
   const int per = (B + kThreads - 1) / kThreads;
   const int e0 = min(B, (int)threadIdx.x * per), e1 = min(B, e0 + per);
   auto members = [&](int b) { return min(min(span, gs[group[b] + 1] - b), B - b); };
-  auto width = [&](int b) { return members(b) > p.MB ? 2 : 1; };
   auto prefix_tiles = [&](int b) { return (most[b] + kTile - 1) / kTile; };
   auto own_tiles = [&](int b) {
     const int g = group[b];
     if (g < 0 || seen[b] <= pl[g]) return 0;
     return (seen[b] - pl[g] / kPageTokens * kPageTokens + kTile - 1) / kTile;
   };
-  int v[4] = {0, 0, 0, 0}, below[4], total[4];     // prefix steps, prefix units, own tiles, own units
+  int v[4] = {0, 0, 0, 0}, below[4], total[4];     // prefix tiles, prefix units, own tiles, own units
   for (int b = e0; b < e1; ++b) {
     const int np = prefix_tiles(b), no = own_tiles(b);
-    if (np) {
-      v[0] += np * width(b);
-      v[1] += 1;
-    }
+    v[0] += np;
+    v[1] += np > 0;
     v[2] += no;
     v[3] += no > 0;
   }
   scan4(s, v, below, total);
   {
-    int steps = below[0], tiles = below[2], units = below[3];
+    int shared = below[0], tiles = below[2], units = below[3];
     for (int b = e0; b < e1; ++b) {
-      ppre[b] = steps;
+      ppre[b] = shared;
       pre[b] = tiles;
       cnt[b] = units;
       const int np = prefix_tiles(b), no = own_tiles(b);
-      if (np) steps += np * width(b);
+      shared += np;
       tiles += no;
       units += no > 0;
     }
@@ -529,7 +528,7 @@ __device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip,
         e.group = g;
         e.prefix_tiles = prefix_tiles(e.lead);
         if (e.prefix_tiles) {
-          e.prefix_width = width(e.lead);
+          e.dual = members(e.lead) > p.MB;
           e.prefix_at = p.Hkv * ppre[e.lead];
         }
         e.own_tiles = own_tiles(b);
@@ -551,12 +550,12 @@ __device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip,
     for (int b = e0; b < e1; ++b) {
       const int nt = prefix_tiles(b);
       if (nt == 0) continue;
-      const int w = width(b), at = p.Hkv * ppre[b];
-      if (at < r1 && at + p.Hkv * nt * w > r0) {
-        for (int h = max(0, (r0 - at) / (nt * w)); h < p.Hkv; ++h) {
-          const int us = at + h * nt * w;
+      const int at = p.Hkv * ppre[b];
+      if (at < r1 && at + p.Hkv * nt > r0) {
+        for (int h = max(0, (r0 - at) / nt); h < p.Hkv; ++h) {
+          const int us = at + h * nt;
           if (us >= r1) break;
-          const int t0 = max(0, (r0 - us + w - 1) >> (w - 1)), t1 = min(nt, (r1 - us + w - 1) >> (w - 1));
+          const int t0 = max(0, r0 - us), t1 = min(nt, r1 - us);
           if (t1 > t0) emit(true, b, h, us, nt, t0, t1, units + h);
         }
       }
@@ -1262,13 +1261,16 @@ __device__ __noinline__ void row_alone(const AttnParams& p, int b, int hq, int g
 // Adds up a row's partial results: prefix shares, then shares of its own
 // tokens, in a fixed order.  W warps per (entry, query head), HD / 32 columns
 // per lane.
+template <int W>
+constexpr int kJoinWarps = W > 4 ? W : 4;   // of a block
+
 template <typename T, int HD, int W>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps<W>) join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int C = HD / 32;
-  __shared__ float s_acc[4][HD];
-  __shared__ float2 s_ml[4];
+  __shared__ float s_acc[W > 1 ? W : 1][HD];
+  __shared__ float2 s_ml[W > 1 ? W : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % W;
-  const int row = (int)blockIdx.x * (4 / W) + warp / W;
+  const int row = (int)blockIdx.x * (kJoinWarps<W> / W) + warp / W;
   const int b = row / p.Hq, hq = row % p.Hq, h = hq / p.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1283,10 +1285,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
   for (int kind = 0; kind < 2; ++kind) {
     const int nt = kind == 0 ? e.prefix_tiles : e.own_tiles;
     if (nt == 0) continue;
-    const bool dual = kind == 0 && e.prefix_width == 2;
-    const int w = dual ? 2 : 1;
-    const int at = kind == 0 ? e.prefix_at + h * nt * w : e.own_at + h * e.own_stride;
-    const int c0 = line.block_of(at), c1 = line.block_of(at + w * (nt - 1));
+    const bool dual = kind == 0 && e.dual;
+    const int at = kind == 0 ? e.prefix_at + h * nt : e.own_at + h * e.own_stride;
+    const int c0 = line.block_of(at), c1 = line.block_of(at + nt - 1);
     const bool whole = c0 == c1;
     // the row's place among its unit's rows
     const int j = kind == 0 ? b - e.lead : b;
@@ -1298,13 +1299,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
       const int c = c0 + (dual ? x : x >> 1), stream = dual ? half : x & 1;
       size_t at_row = 0;
       float2 ml = make_float2(0.0f, 0.0f);
-      bool some = x < n;
-      if (some && dual && !whole) {
-        // a stretch of one step may hold no tile of two
-        const int t0 = max(0, (line.start(c) - at + 1) >> 1), t1 = min(nt, (line.start(c + 1) - at + 1) >> 1);
-        some = t0 < t1;
-      }
-      if (some) {
+      if (x < n) {
         at_row = whole ? whole_row(p, kind, dual ? 0 : stream, b, hq)
                        : ((size_t)(2 * c + (c == c0 ? 1 : 0)) * 2 + stream) * kRows + r;
         ml = p.part_ml[at_row];
@@ -1321,23 +1316,35 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnP
 #pragma unroll
       for (int i = 0; i < C; ++i) acc[i] *= fo;
       const int shares = min(32, (n - i0 + W - 1) / W);
-#pragma unroll 4
-      for (int i = 0; i < shares; ++i) {
-        const float fi = __shfl_sync(kFull, f, i);
-        l = fmaf(__shfl_sync(kFull, ml.y, i), fi, l);
-        const float* src = p.part + __shfl_sync(kFull, (unsigned long long)at_row, i) * HD + lane * C;
-        if (fi == 0.0f) continue;
-        if constexpr (C == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          acc[0] = fmaf(v.x, fi, acc[0]);
-          acc[1] = fmaf(v.y, fi, acc[1]);
-          acc[2] = fmaf(v.z, fi, acc[2]);
-          acc[3] = fmaf(v.w, fi, acc[3]);
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          acc[0] = fmaf(v.x, fi, acc[0]);
-          acc[1] = fmaf(v.y, fi, acc[1]);
+      // eight shares' rows on their way at once
+      for (int i1 = 0; i1 < shares; i1 += 8) {
+        float fi[8], v[8][C];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          fi[u] = __shfl_sync(kFull, f, i1 + u);       // 0 behind the last
+          const float li = __shfl_sync(kFull, ml.y, i1 + u);
+          const float* src = p.part + __shfl_sync(kFull, (unsigned long long)at_row, i1 + u) * HD + lane * C;
+#pragma unroll
+          for (int k = 0; k < C; ++k) v[u][k] = 0.0f;
+          if (fi[u] != 0.0f) {
+            l = fmaf(li, fi[u], l);
+            if constexpr (C == 4) {
+              const float4 t = *reinterpret_cast<const float4*>(src);
+              v[u][0] = t.x;
+              v[u][1] = t.y;
+              v[u][2] = t.z;
+              v[u][3] = t.w;
+            } else {
+              const float2 t = *reinterpret_cast<const float2*>(src);
+              v[u][0] = t.x;
+              v[u][1] = t.y;
+            }
+          }
         }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+          for (int k = 0; k < C; ++k) acc[k] = fmaf(v[u][k], fi[u], acc[k]);
       }
     }
   }
@@ -1414,7 +1421,7 @@ int sm_count(int device) {
   return count[device];
 }
 
-// Rows up to which four warps join one: few rows have many shares each.
+// Rows up to which eight warps join one: few rows have many shares each.
 constexpr unsigned kWideJoin = 2048;
 
 constexpr int kMaxBlocks = 160;      // at least the device's multiprocessors
@@ -1480,7 +1487,7 @@ cudaError_t launch_attention(const AttnParams& p, const CUtensorMap* maps, int d
              maps[2], maps[3]);
   if (e != cudaSuccess) return e;
   const unsigned rows = (unsigned)(p.B * p.Hq);
-  if (rows <= kWideJoin) return launch(join_kernel<T, HD, 4>, rows, 128, 0, st, p);
+  if (rows <= kWideJoin) return launch(join_kernel<T, HD, 8>, rows, 256, 0, st, p);
   return launch(join_kernel<T, HD, 1>, (rows + 3) / 4, 128, 0, st, p);
 }
 
