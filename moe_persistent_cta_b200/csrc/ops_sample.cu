@@ -15,14 +15,18 @@
 // Bound: one read of the logits.  A cluster of up to 8 blocks holds a row in
 // its shared memory, so the passes below touch memory once.  The cut is found
 // by one of three ways:
-//  * top_k up to 64 x blocks: the k-th largest of the maxima of as many groups
-//    of tokens is a logit that at least k tokens reach, and hardly more than
-//    k; those are gathered in one block and sorted, which settles everything.
-//  * top_p alone: a histogram of the distance to the largest logit brackets
-//    the weight of the tokens down to each bin within 1e-5, so the cut lies in
-//    one bin or two; their tokens are gathered and sorted.
+//  * top_k up to 512: the k-th largest of the maxima of 512 groups of tokens is a
+//    logit that at least k tokens reach, and hardly more than k; those are
+//    gathered in one block and ordered, which settles everything.
+//  * top_p alone: the range of logits is narrowed by a factor of 16 at a time by
+//    32-bit sums of the weights, until few tokens are left about the cut; they are
+//    gathered and ordered, and 64-bit sums say which is the last, or that it is
+//    not among them.
 //  * otherwise (large top_k, very many equal logits): the range of keys is
 //    split in four, again and again, by exact sums.
+// Few tokens are ordered by counting, for each, the larger ones: all threads read
+// the same word at a time, and there is no chain of barriers (1024 tokens: 7.9 us
+// by a bitonic sort).
 #include <cooperative_groups.h>
 
 #include "ops_common.cuh"
@@ -37,9 +41,8 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kList = 2048;          // tokens that can be gathered and sorted
-constexpr int kBins = 2048;          // histogram of the distance to the largest
-constexpr int kGroups = kThreads / 8;   // groups of a block whose maxima are kept
+constexpr int kList = 2 * kThreads;  // tokens that can be gathered and ordered
+constexpr int kBins = kWarps;        // parts of a range of logits, one per warp
 
 struct SampleParams {
   int B, V;
@@ -84,27 +87,28 @@ __device__ __forceinline__ __half store_clean<__half>(__half x) {
 struct Exchange {
   double val[2][kMaxCluster][3];
   unsigned long long key[2][kMaxCluster];
+  float bin[2][kMaxCluster][kBins];
 };
 
 struct Shared {
-  unsigned long long list[kList];    // gathered tokens, (key << 32) | ~id
   union {
     struct {
-      uint32_t count[kBins];         // tokens of a bin
-      uint32_t part[kBins];          // sum of their places in it, in 1/256ths
-    } hist;
-    struct {
-      double w[kThreads];            // the draw among sorted tokens
-      int id[kThreads];
-    } draw;
+      unsigned long long list[kList];      // gathered tokens, (key << 32) | ~id
+      unsigned long long sorted[kList];    // in descending order
+      struct {
+        double w[kThreads];
+        int id[kThreads], by_id[kThreads];
+      } draw;                              // the draw among sorted tokens
+    };
+    float bins[kBins][kThreads];           // sums of weights, each thread its own
   };
   double exp2_tab[256];              // 2^(j / 256)
-  uint32_t group_max[kMaxCluster * kGroups];
+  uint32_t group_max[kThreads];
   double warp_val[kWarps][3];
   unsigned long long warp_key[kWarps];
   Exchange ex;
-  uint32_t cut, cut_id;              // handed round by the sorting block
-  int n_list, first_bin, last_bin, picked;
+  uint32_t cut, cut_id;              // handed round by the ordering block
+  int n_list, picked;
 };
 
 // exp(z) for z = d / T <= 0, d = x - max: with y = d (256 / ln 2) / T = n + r,
@@ -211,6 +215,19 @@ class Cluster {
     return best;
   }
 
+  // Sums a block's parts (one per warp, in its lane 0) over the cluster in a
+  // fixed order; lane i of every warp gets part i.
+  __device__ float sum_bins(float mine) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane < size_) *remote(&s_->ex.bin[turn_][rank_][warp], lane) = mine;
+    sync();
+    float t = 0.0f;
+    if (lane < kBins)
+      for (int r = 0; r < size_; ++r) t += s_->ex.bin[turn_][r][lane];
+    turn_ ^= 1;
+    return t;
+  }
+
   __device__ void sync() {
     if (size_ == 1)
       __syncthreads();
@@ -289,8 +306,8 @@ __device__ uint32_t find_cut(Cluster& cl, const Row<T>& row, uint32_t floor_key,
   return (uint32_t)lo;
 }
 
-// Sum of `v` over the block's lower threads.
-__device__ double below_in_block(Shared* s, double v) {
+// Sum of `v` over the block's lower threads; *all: over all of them.
+__device__ double below_in_block(Shared* s, double v, double* all = nullptr) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double inc = v;
 #pragma unroll
@@ -302,10 +319,39 @@ __device__ double below_in_block(Shared* s, double v) {
   __syncthreads();
   if (lane == 31) s->warp_val[warp][0] = inc;
   __syncthreads();
-  double base = 0.0;
-  for (int w = 0; w < warp; ++w) base += s->warp_val[w][0];
+  double base = 0.0, sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) base = sum;
+    sum += s->warp_val[w][0];
+  }
   __syncthreads();
+  if (all) *all = sum;
   return lane == 0 ? base : base + exc;
+}
+
+// Weights of the tokens [from, to) of this thread that `want` picks (0 for the
+// others), four at a time so that their chains overlap: take(i, weight) in order.
+template <typename T, typename F, typename G>
+__device__ __forceinline__ void weigh(const Row<T>& row, F want, G take) {
+  for (int i = row.lo; i < row.hi; i += 4) {
+    float x[4];
+    bool in[4], any = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      in[e] = i + e < row.hi;
+      x[e] = in[e] ? to_float(row.vals[i + e]) : row.mx;
+      in[e] = in[e] && want(x[e], row.id0 + i + e);
+      any |= in[e];
+    }
+    if (!any) continue;
+    double w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = row.weight(x[e]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (in[e]) take(i + e, w[e]);
+  }
 }
 
 // Id of the rank-th (from 1) token, in id order, whose key is `key`.
@@ -324,28 +370,21 @@ __device__ uint32_t nth_equal(Cluster& cl, Shared* s, const Row<T>& row, uint32_
   return (uint32_t)(cl.max_key(found) - 1ull);
 }
 
-// Sorts s->list[0 .. n) in descending order (n <= kList); ends with a barrier.
-// Bitonic; steps whose pairs lie within 64 entries stay inside a warp.
-__device__ void sort_list(Shared* s, int n) {
-  int size = 64;
-  while (size < n) size *= 2;
-  for (int i = n + threadIdx.x; i < size; i += kThreads) s->list[i] = 0;
+// s->sorted: s->list[0 .. n) in descending order (n <= kList, no two alike);
+// ends with a barrier.
+__device__ void order_list(Shared* s, int n) {
+  if (threadIdx.x == 0 && n < kList) s->list[n] = 0;
   __syncthreads();
-  for (int k = 2; k <= size; k *= 2) {
-    for (int j = k / 2; j > 0; j /= 2) {
-      for (int q = threadIdx.x; q < size / 2; q += kThreads) {
-        const int a = 2 * q - (q & (j - 1)), b = a + j;
-        const unsigned long long x = s->list[a], y = s->list[b];
-        if ((x < y) == ((a & k) == 0)) {
-          s->list[a] = y;
-          s->list[b] = x;
-        }
-      }
-      if (j > 32 || (j == 1 && k >= 64))
-        __syncthreads();
-      else
-        __syncwarp();
+  const ulonglong2* two = reinterpret_cast<const ulonglong2*>(s->list);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const unsigned long long mine = s->list[i];
+    int larger = 0;
+#pragma unroll 8
+    for (int k = 0; k < (n + 1) / 2; ++k) {
+      const ulonglong2 v = two[k];
+      larger += (v.x > mine) + (v.y > mine);
     }
+    s->sorted[larger] = mine;
   }
   __syncthreads();
 }
@@ -368,7 +407,7 @@ __device__ void gather(Shared* s, const Row<T>& row, F want) {
 }
 
 // Collects the lists of all blocks, behind a cluster barrier, in block 0,
-// sorted there.  Returns how many tokens there are; if more than kList, nothing
+// ordered there.  Returns how many tokens there are; if more than kList, nothing
 // is collected.  After its own cluster barrier block 0 reads no other's memory.
 __device__ int collect(Cluster& cl, Shared* s) {
   int total = 0, base = 0;
@@ -386,14 +425,14 @@ __device__ int collect(Cluster& cl, Shared* s) {
     }
   }
   cl.sync();
-  if (total <= kList && cl.rank() == 0) sort_list(s, total);
+  if (total <= kList && cl.rank() == 0) order_list(s, total);
   return total;
 }
 
-// Sorted tokens of a thread: four consecutive ones.
+// Ordered tokens of a thread: consecutive ones.
 constexpr int kEach = kList / kThreads;
 
-// Block 0, with the list sorted: how many of the first n tokens are kept by
+// Block 0, with the list ordered: how many of the first n tokens are kept by
 // a limit on the sum before each, starting from `above`: `target`, or top_p of
 // the n tokens' sum where target is negative.  *all: the sum behind them.
 template <typename T>
@@ -403,14 +442,12 @@ __device__ int keep_sorted(Shared* s, const Row<T>& row, int n, float top_p, dou
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const int i = kEach * (int)threadIdx.x + e;
-    w[e] = i < n ? row.weight(value_of((uint32_t)(s->list[i] >> 32))) : 0.0;
+    w[e] = i < n ? row.weight(value_of((uint32_t)(s->sorted[i] >> 32))) : 0.0;
     mine += w[e];
   }
-  double before = above + below_in_block(s, mine);
-  if (threadIdx.x == kThreads - 1) s->warp_val[0][1] = before + mine;
-  if (threadIdx.x == 0) s->n_list = 0;
-  __syncthreads();
-  *all = s->warp_val[0][1];
+  if (threadIdx.x == 0) s->n_list = 0;       // behind the scan's barriers
+  double before = above + below_in_block(s, mine, all);
+  *all += above;
   if (target < 0.0) target = (double)top_p * *all;
   int keep = 0;
 #pragma unroll
@@ -427,117 +464,118 @@ __device__ int keep_sorted(Shared* s, const Row<T>& row, int n, float top_p, dou
   return s->n_list;
 }
 
-// The draw among the first `keep` (1 .. kThreads) tokens of the sorted list, one
-// per thread: each one's running sum over the ids up to its own, added in the
-// order of the list.  True in the thread that holds the drawn token.
+// The draw among the first `keep` (1 .. kThreads) of the ordered tokens, one per
+// thread: put in the order of their ids, their running sums say which.  True in
+// the thread that holds the drawn token.
 template <typename T>
 __device__ bool draw_sorted(Shared* s, const Row<T>& row, int keep, float min_p, float u, int* token,
                             float* logprob) {
-  const bool have = (int)threadIdx.x < keep;
+  const int i = threadIdx.x;
   double w = 0.0;
   int id = 0x7fffffff;
-  if (have) {
-    const unsigned long long e = s->list[threadIdx.x];
+  if (i < keep) {
+    const unsigned long long e = s->sorted[i];
     w = row.weight(value_of((uint32_t)(e >> 32)));
-    if (threadIdx.x > 0 && w < (double)min_p) w = 0.0;
+    if (i > 0 && w < (double)min_p) w = 0.0;
     id = (int)~(uint32_t)e;
   }
-  s->draw.w[threadIdx.x] = w;
-  s->draw.id[threadIdx.x] = id;
-  if (threadIdx.x == 0) s->picked = 0x7fffffff;
+  s->draw.id[i] = id;
+  if (i == 0) s->picked = 0x7fffffff;
   __syncthreads();
-  double upto = 0.0, z = 0.0;
+  if (i < keep) {
+    int lower = 0;
+    const int4* four = reinterpret_cast<const int4*>(s->draw.id);
 #pragma unroll 4
-  for (int j = 0; j < keep; ++j) {
-    const double wj = s->draw.w[j];
-    z += wj;
-    if (s->draw.id[j] <= id) upto += wj;
+    for (int k = 0; k < (keep + 3) / 4; ++k) {
+      const int4 v = four[k];
+      lower += (v.x < id) + (v.y < id) + (v.z < id) + (v.w < id);
+    }
+    s->draw.w[lower] = w;
+    s->draw.by_id[lower] = id;
   }
-  if (have && w > 0.0 && upto > (double)u * z) atomicMin(&s->picked, id);
+  __syncthreads();
+  w = i < keep ? s->draw.w[i] : 0.0;
+  double z;
+  const double upto = below_in_block(s, w, &z) + w;
+  if (w > 0.0 && upto > (double)u * z) atomicMin(&s->picked, i);
   __syncthreads();
   if (s->picked == 0x7fffffff) {     // by rounding: the last one, then
     __syncthreads();
-    if (threadIdx.x == 0) s->picked = -1;
+    if (i == 0) s->picked = -1;
     __syncthreads();
-    if (have && w > 0.0) atomicMax(&s->picked, id);
+    if (w > 0.0) atomicMax(&s->picked, i);
     __syncthreads();
   }
-  if (!have || id != s->picked) return false;
-  *token = id;
+  if (i != s->picked) return false;
+  *token = s->draw.by_id[i];
   *logprob = (float)log(w / z);
   return true;
 }
 
-// The cut of top_p over all tokens, by the histogram.  False if it has to be
-// found another way (the same in every thread of the cluster).
+// The cut of top_p over all tokens, by narrowing.  False if it has to be found
+// another way (the same in every thread of the cluster).
 template <typename T>
-__device__ bool cut_by_bins(Cluster& cl, Shared* s, const Row<T>& row, int V, float top_p, float temp,
-                            uint32_t* cut, uint32_t* cut_id) {
-  // Tokens further than `reach` below the largest (in exponents) weigh less than
-  // V exp(-reach) = (1 - top_p) / e of it together: the cut is not among them.
-  const float reach = logf((float)V / (1.0f - top_p)) + 1.0f;
-  const float scale = (float)kBins / (reach * temp), step = reach / (float)kBins;
-  for (int i = threadIdx.x; i < kBins; i += kThreads) s->hist.count[i] = s->hist.part[i] = 0;
-  __syncthreads();
-  double sum = 0.0;
-  for (int i = row.lo; i < row.hi; ++i) {
-    const float x = to_float(row.vals[i]);
-    const float place = (row.mx - x) * scale;
-    if (place < (float)kBins) {
-      const int bin = (int)place;
-      atomicAdd(&s->hist.count[bin], 1u);
-      atomicAdd(&s->hist.part[bin], (uint32_t)((place - (float)bin) * 256.0f));
-    }
-    sum += row.weight(x);
-  }
-  double t[3];
+__device__ bool narrow_cut(Cluster& cl, Shared* s, const Row<T>& row, int V, float top_p, float temp,
+                           uint32_t* cut, uint32_t* cut_id) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double sum = 0.0, t[3];
+  weigh(row, [](float, int) { return true; }, [&](int, double w) { sum += w; });
   cl.sum3(sum, 0.0, 0.0, t);
   const double target = (double)top_p * t[0];
-  // A bin's weight lies between n exp(-mean) and that times 1 + step^2 / 8; the
-  // mean is known to 1/256 of a bin; places are rounded to 2^-12 of one.
-  const double slack = (double)step * (1.0 / 256 + step / 8 + 1.0 / 4096) + 1e-6;
-  constexpr int kOwn = kBins / kThreads;
-  uint32_t count[kOwn] = {}, part[kOwn] = {};
-  static_assert(kOwn == 4, "one 16-byte load per block");
-  for (int r = 0; r < cl.size(); ++r) {
-    const uint4 c = reinterpret_cast<const uint4*>(cl.remote(s->hist.count, r))[threadIdx.x];
-    const uint4 q = reinterpret_cast<const uint4*>(cl.remote(s->hist.part, r))[threadIdx.x];
-    count[0] += c.x; count[1] += c.y; count[2] += c.z; count[3] += c.w;
-    part[0] += q.x; part[1] += q.y; part[2] += q.z; part[3] += q.w;
-  }
-  double upto[kOwn], mine = 0.0;
+  // Tokens further than `reach` below the largest (in exponents) weigh less than
+  // V exp(-reach) = (1 - top_p) / e of it together: the cut is not among them.
+  const float reach = logf((float)V / (1.0f - top_p)) + 1.0f, rate = 1.4426950f / temp;
+  float lo = 0.0f, width = reach * temp;     // the range: distances to the largest
+  float over = 0.0f;                         // weight before it
+  for (int level = 0;; ++level) {
+    const float scale = (float)kBins / width;
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    const float mean = count[i] ? (float)part[i] / (256.0f * (float)count[i]) : 0.0f;
-    mine += (double)count[i] * exp(-(double)step * ((double)(kOwn * threadIdx.x + i) + (double)mean));
-    upto[i] = mine;
-  }
-  if (threadIdx.x == 0) s->first_bin = s->last_bin = kBins;
-  const double below = below_in_block(s, mine);
+    for (int b = 0; b < kBins; ++b) s->bins[b][threadIdx.x] = 0.0f;
+    for (int i = row.lo; i < row.hi; ++i) {
+      const float d = row.mx - to_float(row.vals[i]), place = (d - lo) * scale;
+      if (place >= 0.0f && place < (float)kBins) s->bins[(int)place][threadIdx.x] += exp2f(-d * rate);
+    }
+    __syncthreads();
+    float part = 0.0f;                       // each warp adds up one bin
 #pragma unroll
-  for (int i = kOwn - 1; i >= 0; --i) {
-    const int bin = kOwn * threadIdx.x + i;
-    if ((below + upto[i]) * (1.0 + slack) >= target) atomicMin(&s->first_bin, bin);
-    if ((below + upto[i]) * (1.0 - slack) >= target) atomicMin(&s->last_bin, bin);
+    for (int k = 0; k < kThreads; k += 32) part += s->bins[warp][k + lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kFull, part, o);
+    const float bin = cl.sum_bins(part);
+    float upto = bin;
+#pragma unroll
+    for (int o = 1; o < kBins; o <<= 1) {
+      const float up = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += up;
+    }
+    // 32-bit weights and their sums are good to 1e-5
+    const float reached = over + upto, want = (float)target;
+    const uint32_t maybe = __ballot_sync(kFull, lane < kBins && reached * (1.0f + 1e-5f) >= want);
+    const uint32_t surely = __ballot_sync(kFull, lane < kBins && reached * (1.0f - 1e-5f) >= want);
+    if (surely == 0) return false;
+    const int first = __ffs(maybe) - 1, last = __ffs(surely) - 1;
+    const float here = __shfl_sync(kFull, upto, last) - (first ? __shfl_sync(kFull, upto, max(first - 1, 0)) : 0.0f);
+    if (first) over += __shfl_sync(kFull, upto, first - 1);
+    lo += (float)first / scale;
+    width = (float)(last - first + 1) / scale;
+    // every token of the range weighs at least 2^(-rate (lo + width))
+    if (here * exp2f(rate * (lo + width)) < 0.75f * (float)kList || level == 4) break;
   }
-  __syncthreads();
-  const int first = s->first_bin, last = s->last_bin;
-  if (last >= kBins) return false;
+  // a little wider, by more than the places' rounding
+  const float slack = 1e-6f * (fabsf(row.mx) + lo + width);
+  const float from = lo - slack, to = lo + width + slack;
   if (threadIdx.x == 0) s->n_list = 0;
-  __syncthreads();
+  __syncthreads();                           // also: the bins, in the list's memory, have been read
   double above = 0.0;
   for (int i = row.lo; i < row.hi; ++i) {
-    const float x = to_float(row.vals[i]);
-    const float place = (row.mx - x) * scale;
-    if (!(place < (float)(last + 1))) continue;
-    if (place < (float)first) {
-      above += row.weight(x);
-    } else {
+    const float x = to_float(row.vals[i]), d = row.mx - x;
+    if (d >= from && d < to) {
       const int at = atomicAdd(&s->n_list, 1);
       if (at < kList)
         s->list[at] = ((unsigned long long)key_of(x) << 32) | (uint32_t)~(uint32_t)(row.id0 + i);
     }
   }
+  weigh(row, [&](float x, int) { return row.mx - x < from; }, [&](int, double w) { above += w; });
   cl.sum3(above, 0.0, 0.0, t);       // behind its barriers every list is whole
   const int n = collect(cl, s);
   if (n > kList) return false;
@@ -547,7 +585,7 @@ __device__ bool cut_by_bins(Cluster& cl, Shared* s, const Row<T>& row, int V, fl
     if ((int)threadIdx.x < cl.size()) {
       // the cut has to lie among these tokens
       const bool found = keep > 0 && (keep < n || all >= target);
-      const unsigned long long e = found ? s->list[keep - 1] : 0ull;
+      const unsigned long long e = found ? s->sorted[keep - 1] : 0ull;
       *cl.remote(&s->cut, threadIdx.x) = (uint32_t)(e >> 32);
       *cl.remote(&s->cut_id, threadIdx.x) = (uint32_t)~(uint32_t)e;
     }
@@ -627,11 +665,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   {
     uint32_t g = top;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(kFull, g, o));
+    for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+      const uint32_t other = __shfl_xor_sync(kFull, g, o);
+      if (o < cluster) g = max(g, other);
+    }
     cl.wait();                       // every block runs: its memory may be written
-    if ((threadIdx.x & 7) == 0)
+    if ((threadIdx.x & (cluster - 1)) == 0)
       for (int r = 0; r < cluster; ++r)
-        *cl.remote(&s.group_max[rank * kGroups + threadIdx.x / 8], r) = g;
+        *cl.remote(&s.group_max[(rank * kThreads + threadIdx.x) / cluster], r) = g;
   }
   // also: every block's part, table and maxima are written
   const unsigned long long best =
@@ -662,16 +703,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     bool settled = false;            // block 0 has drawn among the gathered tokens
     double t[3];
     const bool limited = k > 0 && k < p.V;
-    if (limited && k <= kThreads && (k <= cluster * kGroups || p.V <= kList)) {
+    if (limited && k <= kThreads) {
       // the k-th largest of the groups' maxima to 20 bits, rounded down: k
-      // tokens or more reach it.  A small vocabulary is gathered whole.
+      // tokens or more reach it
       uint32_t t0 = 0;
-      if (p.V > kList) {
-        const uint32_t mine = (int)threadIdx.x < cluster * kGroups ? s.group_max[threadIdx.x] : 0;
-        for (int bit = 31; bit >= 12; --bit) {
-          const uint32_t c = t0 | (1u << bit);
-          if (__syncthreads_count(mine >= c) >= k) t0 = c;
-        }
+      const uint32_t mine = s.group_max[threadIdx.x];
+      for (int bit = 31; bit >= 12; --bit) {
+        const uint32_t c = t0 | (1u << bit);
+        if (__syncthreads_count(mine >= c) >= k) t0 = c;
       }
       t0 = max(t0, floor_key);
       gather(&s, row, [&](float x) { return key_of(x) >= t0; });
@@ -697,12 +736,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const uint32_t key = key_of(x);
         return key > cut || (key == cut && (uint32_t)id <= cut_id);
       };
-      if (top_p < 1.0f && (limited || row.inf || !cut_by_bins(cl, &s, row, p.V, top_p, temp, &cut, &cut_id))) {
+      if (top_p < 1.0f && (limited || row.inf || !narrow_cut(cl, &s, row, p.V, top_p, temp, &cut, &cut_id))) {
         double sum = 0.0;
-        for (int i = row.lo; i < row.hi; ++i) {
-          const float x = to_float(vals[i]);
-          if (kept(x, row.id0 + i)) sum += row.weight(x);
-        }
+        weigh(row, kept, [&](int, double w) { sum += w; });
         cl.sum3(sum, 0.0, 0.0, t);
         const double target = (double)top_p * t[0];
         double above, at;
@@ -738,14 +774,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       // the draw, in id order
       double mine = 0.0;
       int last = -1;
-      for (int i = row.lo; i < row.hi; ++i) {
-        const float x = to_float(vals[i]);
-        if (!kept(x, row.id0 + i)) continue;
-        const double w = row.weight(x);
-        if (w < (double)min_p || w == 0.0) continue;
+      weigh(row, kept, [&](int i, double w) {
+        if (w < (double)min_p || w == 0.0) return;
         mine += w;
         last = i;
-      }
+      });
       double under[3];
       cl.sum3(mine, 0.0, 0.0, t, under);
       const double z = t[0], target = (double)u * z;
@@ -757,21 +790,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (last >= 0)
         c = before + mine > target ? (1ull << 62) - place : 1ull + place;
       const unsigned long long won = cl.max_key(c);
-      writer = last >= 0 && c == won;
-      if (writer) {
-        double acc = before;
-        int pick = last;
-        for (int i = row.lo; i <= last; ++i) {
-          const float x = to_float(vals[i]);
-          if (!kept(x, row.id0 + i)) continue;
-          const double w = row.weight(x);
-          if (w < (double)min_p || w == 0.0) continue;
-          acc += w;
-          if (acc > target) {
-            pick = i;
+      // that thread's warp goes through its tokens together
+      const int lane = threadIdx.x & 31;
+      const uint32_t winner = __ballot_sync(kFull, last >= 0 && c == won);
+      writer = false;
+      if (winner) {
+        const int src = __ffs(winner) - 1;
+        const int end = __shfl_sync(kFull, last, src) + 1;
+        double acc = __shfl_sync(kFull, before, src);
+        int pick = end - 1;
+        for (int i0 = __shfl_sync(kFull, row.lo, src); i0 < end; i0 += 32) {
+          const int i = i0 + lane;
+          const float x = i < end ? to_float(vals[i]) : 0.0f;
+          double w = i < end && kept(x, row.id0 + i) ? row.weight(x) : 0.0;
+          if (w < (double)min_p) w = 0.0;
+          double upto = w;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const double up = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += up;
+          }
+          const uint32_t passed = __ballot_sync(kFull, w > 0.0 && acc + upto > target);
+          if (passed) {
+            pick = i0 + __ffs(passed) - 1;
             break;
           }
+          acc += __shfl_sync(kFull, upto, 31);
         }
+        writer = lane == src;
         token = row.id0 + pick;
         logprob = (float)log(row.weight(to_float(vals[pick])) / z);
       }
