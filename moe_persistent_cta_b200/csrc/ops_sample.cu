@@ -108,7 +108,7 @@ struct Shared {
   unsigned long long warp_key[kWarps];
   Exchange ex;
   uint32_t cut, cut_id;              // handed round by the ordering block
-  int n_list, picked;
+  int n_list, kept, picked;
 };
 
 // exp(z) for z = d / T <= 0, d = x - max: with y = d (256 / ln 2) / T = n + r,
@@ -194,6 +194,25 @@ class Cluster {
     turn_ ^= 1;
   }
 
+  // Sums a number over the cluster as above; says whether this is the block at
+  // which the running sum over blocks passes u of the whole, or, if by rounding
+  // none does, the last that adds anything.
+  __device__ bool sum_drawn(double a, float u, double* out, double* below) {
+    const int turn = turn_;
+    sum3(a, 0.0, 0.0, out, below);
+    double upto = 0.0;
+    int at = -1, some = -1;
+    for (int r = 0; r < size_; ++r) {
+      const double v = s_->ex.val[turn][r][0];
+      upto += v;
+      if (v > 0.0) {
+        some = r;
+        if (at < 0 && upto > (double)u * out[0]) at = r;
+      }
+    }
+    return (at >= 0 ? at : some) == rank_;
+  }
+
   // The largest key over the cluster.
   __device__ unsigned long long max_key(unsigned long long k) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -239,18 +258,20 @@ class Cluster {
   __device__ U* remote(U* p, int r) {
     return size_ == 1 ? p : cg::this_cluster().map_shared_rank(p, r);
   }
-  // A barrier in two parts: every block of the cluster has begun.
+  // A barrier in two parts; what a block has read of another's memory before
+  // the first is read before the other block gets past the second.
   __device__ void arrive() {
-    if (size_ > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    __syncwarp();
+    if (size_ > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   __device__ void wait() {
+    __syncwarp();
     if (size_ > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   __device__ int size() const { return size_; }
   __device__ int rank() const { return rank_; }
 
  private:
-
   Shared* s_;
   int rank_, size_;
   int turn_ = 0;
@@ -330,7 +351,20 @@ __device__ double below_in_block(Shared* s, double v, double* all = nullptr) {
   return lane == 0 ? base : base + exc;
 }
 
-// Weights of the tokens [from, to) of this thread that `want` picks (0 for the
+// f(logit, place) for this thread's tokens in order, eight loads ahead.
+template <typename T, typename F>
+__device__ __forceinline__ void each(const Row<T>& row, F f) {
+  for (int i = row.lo; i < row.hi; i += 8) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = i + e < row.hi ? to_float(row.vals[i + e]) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e < row.hi) f(x[e], i + e);
+  }
+}
+
+// Weights of the tokens of this thread that `want` picks (0 for the
 // others), four at a time so that their chains overlap: take(i, weight) in order.
 template <typename T, typename F, typename G>
 __device__ __forceinline__ void weigh(const Row<T>& row, F want, G take) {
@@ -389,44 +423,26 @@ __device__ void order_list(Shared* s, int n) {
   __syncthreads();
 }
 
-// Appends this block's tokens that `want` picks to its list, kList at most;
-// n_list counts all.  Ends with a barrier.
+// Gathers the row's tokens that `want` picks in block 0 of the cluster, kList at
+// most, and orders them there.  Returns how many there are (if more than kList,
+// nothing is ordered); n_list has been 0 in block 0 since an earlier cluster
+// barrier.  Ends behind a cluster barrier that block 0 alone has to wait for
+// (cl.wait(), before it touches n_list or leaves).
 template <typename T, typename F>
-__device__ void gather(Shared* s, const Row<T>& row, F want) {
-  if (threadIdx.x == 0) s->n_list = 0;
-  __syncthreads();
-  for (int i = row.lo; i < row.hi; ++i) {
-    const float x = to_float(row.vals[i]);
+__device__ int gather(Cluster& cl, Shared* s, const Row<T>& row, F want) {
+  int* count = cl.remote(&s->n_list, 0);
+  unsigned long long* list = cl.remote(s->list, 0);
+  each(row, [&](float x, int i) {
     if (want(x)) {
-      const int at = atomicAdd(&s->n_list, 1);
-      if (at < kList)
-        s->list[at] = ((unsigned long long)key_of(x) << 32) | (uint32_t)~(uint32_t)(row.id0 + i);
+      const int at = atomicAdd(count, 1);
+      if (at < kList) list[at] = ((unsigned long long)key_of(x) << 32) | (uint32_t)~(uint32_t)(row.id0 + i);
     }
-  }
-  __syncthreads();
-}
-
-// Collects the lists of all blocks, behind a cluster barrier, in block 0,
-// ordered there.  Returns how many tokens there are; if more than kList, nothing
-// is collected.  After its own cluster barrier block 0 reads no other's memory.
-__device__ int collect(Cluster& cl, Shared* s) {
-  int total = 0, base = 0;
-  for (int r = 0; r < cl.size(); ++r) {
-    const int n = *cl.remote(&s->n_list, r);
-    total += n;
-  }
-  if (total <= kList && cl.rank() == 0) {
-    base = s->n_list;
-    for (int r = 1; r < cl.size(); ++r) {
-      const int n = *cl.remote(&s->n_list, r);
-      const unsigned long long* src = cl.remote(s->list, r);
-      for (int i = threadIdx.x; i < n; i += kThreads) s->list[base + i] = src[i];
-      base += n;
-    }
-  }
+  });
   cl.sync();
-  if (total <= kList && cl.rank() == 0) order_list(s, total);
-  return total;
+  const int n = *count;
+  cl.arrive();
+  if (n <= kList && cl.rank() == 0) order_list(s, n);
+  return n;
 }
 
 // Ordered tokens of a thread: consecutive ones.
@@ -445,7 +461,7 @@ __device__ int keep_sorted(Shared* s, const Row<T>& row, int n, float top_p, dou
     w[e] = i < n ? row.weight(value_of((uint32_t)(s->sorted[i] >> 32))) : 0.0;
     mine += w[e];
   }
-  if (threadIdx.x == 0) s->n_list = 0;       // behind the scan's barriers
+  if (threadIdx.x == 0) s->kept = 0;         // behind the scan's barriers
   double before = above + below_in_block(s, mine, all);
   *all += above;
   if (target < 0.0) target = (double)top_p * *all;
@@ -459,9 +475,9 @@ __device__ int keep_sorted(Shared* s, const Row<T>& row, int n, float top_p, dou
   // what is kept is a prefix, so the number says which
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) keep += __shfl_xor_sync(kFull, keep, o);
-  if ((threadIdx.x & 31) == 0 && keep) atomicAdd(&s->n_list, keep);
+  if ((threadIdx.x & 31) == 0 && keep) atomicAdd(&s->kept, keep);
   __syncthreads();
-  return s->n_list;
+  return s->kept;
 }
 
 // The draw among the first `keep` (1 .. kThreads) of the ordered tokens, one per
@@ -531,10 +547,10 @@ __device__ bool narrow_cut(Cluster& cl, Shared* s, const Row<T>& row, int V, flo
     const float scale = (float)kBins / width;
 #pragma unroll
     for (int b = 0; b < kBins; ++b) s->bins[b][threadIdx.x] = 0.0f;
-    for (int i = row.lo; i < row.hi; ++i) {
-      const float d = row.mx - to_float(row.vals[i]), place = (d - lo) * scale;
+    each(row, [&](float x, int) {
+      const float d = row.mx - x, place = (d - lo) * scale;
       if (place >= 0.0f && place < (float)kBins) s->bins[(int)place][threadIdx.x] += exp2f(-d * rate);
-    }
+    });
     __syncthreads();
     float part = 0.0f;                       // each warp adds up one bin
 #pragma unroll
@@ -559,25 +575,20 @@ __device__ bool narrow_cut(Cluster& cl, Shared* s, const Row<T>& row, int V, flo
     lo += (float)first / scale;
     width = (float)(last - first + 1) / scale;
     // every token of the range weighs at least 2^(-rate (lo + width))
-    if (here * exp2f(rate * (lo + width)) < 0.75f * (float)kList || level == 4) break;
+    // (ordering n tokens takes n^2: 1000 as long as three more rounds)
+    if (here * exp2f(rate * (lo + width)) < 256.0f || level == 5) break;
   }
   // a little wider, by more than the places' rounding
   const float slack = 1e-6f * (fabsf(row.mx) + lo + width);
   const float from = lo - slack, to = lo + width + slack;
-  if (threadIdx.x == 0) s->n_list = 0;
-  __syncthreads();                           // also: the bins, in the list's memory, have been read
   double above = 0.0;
-  for (int i = row.lo; i < row.hi; ++i) {
-    const float x = to_float(row.vals[i]), d = row.mx - x;
-    if (d >= from && d < to) {
-      const int at = atomicAdd(&s->n_list, 1);
-      if (at < kList)
-        s->list[at] = ((unsigned long long)key_of(x) << 32) | (uint32_t)~(uint32_t)(row.id0 + i);
-    }
-  }
   weigh(row, [&](float x, int) { return row.mx - x < from; }, [&](int, double w) { above += w; });
-  cl.sum3(above, 0.0, 0.0, t);       // behind its barriers every list is whole
-  const int n = collect(cl, s);
+  cl.sum3(above, 0.0, 0.0, t);
+  const int n = gather(cl, s, row, [&](float x) {
+    const float d = row.mx - x;
+    return d >= from && d < to;
+  });
+  cl.wait();
   if (n > kList) return false;
   if (cl.rank() == 0) {
     double all;
@@ -661,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
   }
   for (int i = lead + vecs * VE + threadIdx.x; i < row.n; i += kThreads) vals[i] = take(src[i], i);
+  if (threadIdx.x == 0) s.n_list = 0;
   if (threadIdx.x < 256) s.exp2_tab[threadIdx.x] = exp2((double)threadIdx.x / 256.0);
   {
     uint32_t g = top;
@@ -713,9 +725,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if (__syncthreads_count(mine >= c) >= k) t0 = c;
       }
       t0 = max(t0, floor_key);
-      gather(&s, row, [&](float x) { return key_of(x) >= t0; });
-      cl.sync();
-      const int n = collect(cl, &s);
+      const int n = gather(cl, &s, row, [&](float x) { return key_of(x) >= t0; });
       if (n <= kList) {
         settled = true;
         writer = false;
@@ -725,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           writer = draw_sorted(&s, row, max(keep, 1), min_p, u, &token, &logprob);
         }
       }
+      cl.wait();
     }
     if (limited && !settled) {
       double above, at;
@@ -780,19 +791,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         last = i;
       });
       double under[3];
-      cl.sum3(mine, 0.0, 0.0, t, under);
+      const bool here = cl.sum_drawn(mine, u, t, under);
       const double z = t[0], target = (double)u * z;
-      const double before = under[0] + below_in_block(&s, mine);
-      // the first thread that holds kept tokens and passes the target; by
-      // rounding there may be none, then the last that holds any
-      const uint32_t place = (uint32_t)(rank * kThreads + threadIdx.x);
-      unsigned long long c = 0;
-      if (last >= 0)
-        c = before + mine > target ? (1ull << 62) - place : 1ull + place;
-      const unsigned long long won = cl.max_key(c);
+      // in the one block whose tokens pass the target: the first thread that holds
+      // kept tokens and passes it; by rounding there may be none, then the last
+      // that holds any
+      int won = -1;
+      double before = 0.0;
+      if (here) {
+        before = under[0] + below_in_block(&s, mine);
+        if (threadIdx.x == 0) s.picked = 0x7fffffff;
+        __syncthreads();
+        if (last >= 0) atomicMin(&s.picked, before + mine > target ? (int)threadIdx.x : 2 * kThreads - (int)threadIdx.x);
+        __syncthreads();
+        won = s.picked < kThreads ? s.picked : 2 * kThreads - s.picked;
+      }
       // that thread's warp goes through its tokens together
       const int lane = threadIdx.x & 31;
-      const uint32_t winner = __ballot_sync(kFull, last >= 0 && c == won);
+      const uint32_t winner = __ballot_sync(kFull, (int)threadIdx.x == won);
       writer = false;
       if (winner) {
         const int src = __ffs(winner) - 1;
