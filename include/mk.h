@@ -397,8 +397,10 @@ mk_status mk_rope_append(const mk_rope_append_args* args, void* stream);
  *               mk_prefix_attention_workspace(args); contents do not matter
  * Entries of one sequence with increasing positions are a causal piece of a
  * prompt: give the group a prefix that covers them all.  Group bounds out of
- * order, a position outside the page table or a page id out of range is a
- * device-side fault (the entry or page contributes nothing).  n_q_heads is a
+ * order (then no entry is computed), a position outside the page table (the
+ * entry then sees nothing) or a page id out of range (its keys and values read
+ * as zero) is a device-side fault.  What other entries' tokens hold, infinities
+ * and NaN included, does not reach an entry's row.  n_q_heads is a
  * multiple of n_kv_heads, at most 64 times it; batch is at most 4096.       */
 typedef struct mk_prefix_attention_args {
   int32_t device;
@@ -456,6 +458,45 @@ typedef struct mk_sample_args {
   int32_t* status;
 } mk_sample_args;
 mk_status mk_sample(const mk_sample_args* args, void* stream);
+
+/* mk_decode_step for batches whose entries continue the same prompts: the
+ * pages of a shared prefix are read once per group and layer, not once per
+ * entry.  Per layer the step runs as one launch of the task interpreter (all
+ * operations but attention), mk_rope_append on the layer's projections and
+ * mk_prefix_attention, whose 32-bit result the output projection reads; queries
+ * are rounded to bf16 after the rotation, which mk_decode_step does not do.
+ * Arguments are mk_decode_step's, and
+ *   n_groups    1 .. batch
+ *   group_start int32[n_groups + 1], prefix_lens int32[n_groups], device: as for
+ *               mk_prefix_attention; every entry must be in a group
+ * It pays where reading the prefix dominates: the launches cost more than the
+ * fused step's counters on short ones.  plan_len of the schedule does not limit
+ * the lengths, the page table does.  A fault of the two operators is reported by
+ * mk_check as {code, operator, entry, value, limit}.  The first call after
+ * mk_build_schedule allocates, so it cannot be captured into a graph.        */
+mk_status mk_decode_step_shared(mk_ctx* ctx, const int32_t* tokens, const int32_t* positions,
+                                const int32_t* page_table, const int32_t* seq_lens,
+                                int32_t n_groups, const int32_t* group_start,
+                                const int32_t* prefix_lens, float* logits, void* stream);
+
+/* Sampled decoding: mk_decode_greedy with mk_sample in the place of the largest
+ * logit.  Step i draws with u[i][b], writes the token to out_tokens[i][b] (-1 if
+ * there is nothing to draw) and to tokens[b] (then 0), and advances positions[b]
+ * and seq_lens[b].  The rules are mk_sample's, the same in every step; those
+ * that are NULL do not apply.  n_groups > 0 runs the steps as
+ * mk_decode_step_shared; 0 as mk_decode_step.  Faults surface through mk_check. */
+typedef struct mk_sampling {
+  const float* u;            /* float32[n_steps][batch] */
+  const float* temperature;  /* float32[batch] or NULL */
+  const int32_t* top_k;      /* int32[batch] or NULL */
+  const float *top_p, *min_p;   /* float32[batch] or NULL */
+  float* logprobs;           /* float32[n_steps][batch] or NULL */
+  const int32_t *group_start, *prefix_lens;
+  int32_t n_groups;
+} mk_sampling;
+mk_status mk_decode_sample(mk_ctx* ctx, int32_t n_steps, int32_t* tokens, int32_t* positions,
+                           const int32_t* page_table, int32_t* seq_lens, float* logits,
+                           int32_t* out_tokens, const mk_sampling* how, void* stream);
 
 const char* mk_strerror(mk_status s);
 

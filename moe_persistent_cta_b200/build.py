@@ -19,7 +19,7 @@ INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libmk.so")
 
 SOURCES = ["mk_kernel.cu", "mk_host.cpp", "mk_plan.cpp", "mk_static.cu", "ops_append.cu",
-           "ops_attention.cu", "ops_sample.cu"]
+           "ops_attention.cu", "ops_sample.cu", "ops_step.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

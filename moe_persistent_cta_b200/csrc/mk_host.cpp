@@ -10,10 +10,12 @@
 #include <algorithm>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "mk.h"
 #include "mk_internal.h"
+#include "ops_step.h"
 
 namespace mk {
 cudaError_t launch_interp(const Params& p, int grid, cudaStream_t stream);
@@ -48,6 +50,7 @@ struct mk_ctx {
   void** d_router_bias = nullptr;
   void** d_kpool = nullptr;
   void** d_vpool = nullptr;
+  std::vector<void*> h_kpool, h_vpool;   // the same pointers on the host
   double* d_inv_freq = nullptr;
   int32_t* d_status = nullptr;
   uint32_t* d_counters = nullptr;
@@ -56,6 +59,13 @@ struct mk_ctx {
   bool phases_uploaded = false;
   DevBuf x, actA, qkv, cs, attn_part, attn_o, ofrag, o_part, rlogits, racc, ssacc, route, expert_a, afrag,
       moe_part, amax, trace;
+  // the step with shared prefixes, set up by its first call after a schedule
+  DevBuf shared_desc;      // the fused list, expert jumps relative to their segment
+  DevBuf shared_counters;  // (counter, arrivals a step) of the attention tasks left out
+  DevBuf shared_q, shared_work;
+  std::vector<int> segments;   // segment i is tasks [segments[2 i], segments[2 i + 1]) of the list
+  int n_shared_counters = 0;
+  bool shared_ready = false;
   DevBuf selftest;   // one descriptor + two counters for mk_selftest_timeout
   bool tracing = false;
   // schedule
@@ -180,7 +190,8 @@ void mk_destroy(mk_ctx* c) {
   for (DevBuf* b : {&c->desc, &c->phase_desc, &c->x, &c->actA,
                     &c->qkv, &c->cs, &c->attn_part, &c->attn_o, &c->ofrag, &c->o_part,
                     &c->rlogits, &c->racc, &c->ssacc, &c->route, &c->expert_a, &c->afrag, &c->moe_part,
-                    &c->amax, &c->trace, &c->selftest})
+                    &c->amax, &c->trace, &c->selftest, &c->shared_desc, &c->shared_counters,
+                    &c->shared_q, &c->shared_work})
     release(*b);
   c->plan.release();
   delete c;
@@ -282,6 +293,8 @@ mk_status mk_create(const mk_config* cfg, const mk_tensors* t, int device, mk_ct
     kp[l] = t->k_pool[l];
     vp[l] = t->v_pool[l];
   }
+  c->h_kpool = kp;
+  c->h_vpool = vp;
   auto upload_ptrs = [&](void*** dst, std::vector<void*>& src) -> mk_status {
     MK_CUDA(cudaMalloc(reinterpret_cast<void**>(dst), sizeof(void*) * src.size()));
     MK_CUDA(cudaMemcpy(*dst, src.data(), sizeof(void*) * src.size(), cudaMemcpyHostToDevice));
@@ -410,6 +423,7 @@ mk_status mk_build_schedule(mk_ctx* c, int batch, const int32_t* seq_lens,
   if (cudaMemcpy(c->desc.ptr, plan.desc, (size_t)plan.n_tasks * mk::kDescWords * 4,
                  cudaMemcpyHostToDevice) != cudaSuccess)
     return fail(MK_ERR_CUDA);
+  c->shared_ready = false;
   c->phases_uploaded = false;   // the unfused path builds its phase lists on first use
 
   Params& p = c->base;
@@ -576,6 +590,194 @@ mk_status mk_decode_greedy(mk_ctx* c, int32_t n_steps, int32_t* tokens, int32_t*
   for (int32_t i = 0; i < n_steps; ++i) {
     const Greedy g{tokens, positions, seq_lens, out_tokens + (size_t)i * c->B};
     MK_TRY(launch_step(c, tokens, positions, page_table, seq_lens, logits, stream, false, &g));
+  }
+  return MK_OK;
+}
+
+// The fused list cut at its attention tasks, which are contiguous per layer:
+// what lies between them runs as one launch each.  Those tasks' counter
+// arrivals are added by one kernel ahead of the step.
+static mk_status prepare_shared(mk_ctx* c) try {
+  if (c->shared_ready) return MK_OK;
+  const mk::Plan& plan = c->plan;
+  const int W = mk::kDescWords;
+  std::vector<int32_t> list(plan.desc, plan.desc + (size_t)plan.n_tasks * W);
+  std::vector<int32_t> add(plan.n_counters, 0);
+  c->segments.clear();
+  int start = -1;
+  for (int i = 0; i <= plan.n_tasks; ++i) {
+    const int32_t* w = i < plan.n_tasks ? plan.desc + (size_t)i * W : nullptr;
+    if (w && w[mk::D_OP] != mk::OP_ATTN) {
+      if (start < 0) start = i;
+      if (w[mk::D_OP] == mk::OP_GATEUP || w[mk::D_OP] == mk::OP_DOWN) list[(size_t)i * W + mk::D_C] -= start;
+      continue;
+    }
+    if (start >= 0) {
+      c->segments.push_back(start);
+      c->segments.push_back(i);
+      start = -1;
+    }
+    if (!w) break;
+    for (int k = 0; k < w[mk::D_NSIG]; ++k) add[w[mk::D_S0 + k]] += 1;
+    if (w[mk::D_FLAGS] & mk::F_COMBINE) {
+      add[w[mk::D_X0]] += 1;
+      if (w[mk::D_C] == 0) add[w[mk::D_X2]] += 1;   // by the last of the (token, KV head)'s chunks
+    }
+  }
+  if ((int)c->segments.size() != 2 * (c->shape.L + 1)) return MK_ERR_STATE;
+  std::vector<int32_t> pairs;
+  for (int i = 0; i < plan.n_counters; ++i)
+    if (add[i]) {
+      pairs.push_back(i);
+      pairs.push_back(add[i]);
+    }
+  c->n_shared_counters = (int)pairs.size() / 2;
+  MK_TRY(ensure(c->shared_desc, list.size() * 4));
+  MK_TRY(ensure(c->shared_counters, pairs.size() * 4));
+  MK_TRY(ensure(c->shared_q, (size_t)c->B * c->shape.Hq * c->shape.hd * 2));
+  MK_CUDA(cudaMemcpy(c->shared_desc.ptr, list.data(), list.size() * 4, cudaMemcpyHostToDevice));
+  MK_CUDA(cudaMemcpy(c->shared_counters.ptr, pairs.data(), pairs.size() * 4, cudaMemcpyHostToDevice));
+  c->shared_ready = true;
+  return MK_OK;
+} catch (const std::bad_alloc&) {
+  return MK_ERR_OOM;
+}
+
+static mk_status launch_shared(mk_ctx* c, const int32_t* tokens, const int32_t* positions,
+                               const int32_t* page_table, const int32_t* seq_lens, int32_t n_groups,
+                               const int32_t* group_start, const int32_t* prefix_lens, float* logits,
+                               void* stream) {
+  if (!c) return MK_ERR_INVALID;
+  if (!c->have_schedule) return MK_ERR_STATE;
+  if (!tokens || !positions || !page_table || !seq_lens || !logits) return MK_ERR_INVALID;
+  if (n_groups < 1 || n_groups > c->B || !group_start || !prefix_lens) return MK_ERR_INVALID;
+  MK_CUDA(cudaSetDevice(c->device));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MK_TRY(prepare_shared(c));
+  const Shape& s = c->shape;
+  mk_prefix_attention_args at{};
+  at.device = c->device;
+  at.batch = c->B;
+  at.n_groups = n_groups;
+  at.max_pages = c->max_pages;
+  at.n_pages = s.n_pages;
+  at.n_q_heads = s.Hq;
+  at.n_kv_heads = s.Hkv;
+  at.head_dim = s.hd;
+  at.type = MK_BF16;
+  at.scale = 1.0f / std::sqrt((float)s.hd);
+  at.q = c->shared_q.ptr;
+  at.q_token_stride = (int64_t)s.Hq * s.hd;
+  at.page_table = page_table;
+  at.positions = positions;
+  at.group_start = group_start;
+  at.prefix_lens = prefix_lens;
+  at.status = c->d_status;
+  const size_t work = mk_prefix_attention_workspace(&at);
+  if (work == 0) return MK_ERR_CAPACITY;
+  MK_TRY(ensure(c->shared_work, work));
+  at.workspace = c->shared_work.ptr;
+  at.workspace_bytes = c->shared_work.bytes;
+  mk_rope_append_args ap{};
+  ap.device = c->device;
+  ap.n_tokens = ap.n_rows = c->B;
+  ap.max_pages = c->max_pages;
+  ap.n_pages = s.n_pages;
+  ap.n_q_heads = s.Hq;
+  ap.n_kv_heads = s.Hkv;
+  ap.head_dim = ap.rotary_dim = s.hd;
+  ap.src_type = MK_FP32;
+  ap.dst_type = MK_BF16;
+  ap.magnitude = 1.0f;
+  const int row = (s.Hq + 2 * s.Hkv) * s.hd;
+  ap.q_token_stride = ap.k_token_stride = ap.v_token_stride = row;
+  ap.q_head_stride = ap.k_head_stride = ap.v_head_stride = s.hd;
+  ap.q_out = c->shared_q.ptr;
+  ap.inv_freq = c->d_inv_freq;
+  ap.positions = positions;
+  ap.page_table = page_table;
+  ap.status = c->d_status;
+
+  Params p = c->base;
+  p.tokens = tokens;
+  p.positions = positions;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.logits = logits;
+  p.timeout_cycles = deadline_cycles(c, c->timeout_ns);
+  p.epoch = c->epoch + 1;
+  p.n_ctas = c->plan.n_ctas;
+  MK_CUDA(mk::ops::add_to_counters(c->d_counters, static_cast<const int32_t*>(c->shared_counters.ptr),
+                                   c->n_shared_counters, st));
+  // from here on a step that stops part-way leaves counters short: mk_check's
+  // reset is needed, as after a device error
+  c->epoch += 1;
+  c->last_stream = st;
+  c->launched = true;
+  for (int l = 0; l <= s.L; ++l) {
+    const int from = c->segments[2 * l];
+    p.desc = static_cast<const int32_t*>(c->shared_desc.ptr) + (size_t)from * mk::kDescWords;
+    p.n_tasks = c->segments[2 * l + 1] - from;
+    p.grab = c->plan.grab_phase0 + l;
+    MK_CUDA(mk::launch_interp(p, c->plan.n_ctas, st));
+    if (l == s.L) break;
+    const float* qkv = p.qkv + (size_t)l * c->B * row;
+    ap.q = qkv;
+    ap.k = qkv + (size_t)s.Hq * s.hd;
+    ap.v = qkv + (size_t)(s.Hq + s.Hkv) * s.hd;
+    ap.k_pool = c->h_kpool[l];
+    ap.v_pool = c->h_vpool[l];
+    MK_TRY(mk_rope_append(&ap, stream));
+    at.k_pool = ap.k_pool;
+    at.v_pool = ap.v_pool;
+    mk::ops::StepSink sink;
+    sink.out = p.attn_o + (size_t)l * c->B * s.Hq * s.hd;
+    sink.frag = p.ofrag + (size_t)l * s.Hkv * p.ofrag_bytes;
+    sink.frag_bytes = p.ofrag_bytes;
+    sink.frag_stride = s.Hq / s.Hkv * s.hd + mk::kActPad;
+    MK_TRY(mk::ops::prefix_attention(&at, sink, st));
+  }
+  return MK_OK;
+}
+
+mk_status mk_decode_step_shared(mk_ctx* c, const int32_t* tokens, const int32_t* positions,
+                                const int32_t* page_table, const int32_t* seq_lens, int32_t n_groups,
+                                const int32_t* group_start, const int32_t* prefix_lens, float* logits,
+                                void* stream) {
+  return launch_shared(c, tokens, positions, page_table, seq_lens, n_groups, group_start, prefix_lens,
+                       logits, stream);
+}
+
+mk_status mk_decode_sample(mk_ctx* c, int32_t n_steps, int32_t* tokens, int32_t* positions,
+                           const int32_t* page_table, int32_t* seq_lens, float* logits,
+                           int32_t* out_tokens, const mk_sampling* how, void* stream) {
+  if (!c || !how) return MK_ERR_INVALID;
+  if (n_steps < 0 || (n_steps > 0 && (!out_tokens || !how->u))) return MK_ERR_INVALID;
+  if (!c->have_schedule) return MK_ERR_STATE;
+  mk_sample_args a{};
+  a.device = c->device;
+  a.batch = c->B;
+  a.vocab = c->shape.V;
+  a.type = MK_FP32;
+  a.logits = logits;
+  a.row_stride = c->shape.V;
+  a.temperature = how->temperature;
+  a.top_k = how->top_k;
+  a.top_p = how->top_p;
+  a.min_p = how->min_p;
+  a.status = c->d_status;
+  if (a.vocab > MK_SAMPLE_MAX_VOCAB) return MK_ERR_CAPACITY;
+  for (int32_t i = 0; i < n_steps; ++i) {
+    const size_t at = (size_t)i * c->B;
+    if (how->n_groups > 0)
+      MK_TRY(launch_shared(c, tokens, positions, page_table, seq_lens, how->n_groups, how->group_start,
+                           how->prefix_lens, logits, stream));
+    else
+      MK_TRY(launch_step(c, tokens, positions, page_table, seq_lens, logits, stream, false));
+    a.u = how->u + at;
+    a.tokens = out_tokens + at;
+    a.logprobs = how->logprobs ? how->logprobs + at : nullptr;
+    MK_TRY(mk::ops::sample(&a, tokens, positions, seq_lens, static_cast<cudaStream_t>(stream)));
   }
   return MK_OK;
 }

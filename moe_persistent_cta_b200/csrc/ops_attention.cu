@@ -42,6 +42,7 @@
 #include <mutex>
 
 #include "ops_common.cuh"
+#include "ops_step.h"
 
 namespace mk {
 namespace ops {
@@ -100,6 +101,7 @@ struct AttnParams {
   long long q_stride;
   void* out;
   float* lse;
+  StepSink sink;
   int32_t* status;
 };
 
@@ -1231,6 +1233,18 @@ __device__ __noinline__ void row_alone(const AttnParams& p, int b, int hq, int g
 // Adds up a row's partial results: prefix shares, then shares of its own
 // tokens, in a fixed order.  W warps per (entry, query head), HD / 32 columns
 // per lane.
+// A row's result as the decode step's next operation reads it.
+template <int HD>
+__device__ __forceinline__ void to_step(const AttnParams& p, int b, int hq, const float* o) {
+  constexpr int C = HD / 32;
+  const int lane = threadIdx.x & 31;
+  float* a = p.sink.out + ((size_t)b * p.Hq + hq) * HD + lane * C;
+  float* f = reinterpret_cast<float*>(p.sink.frag + (size_t)(hq / p.G) * p.sink.frag_bytes) +
+             (size_t)b * p.sink.frag_stride + hq % p.G * HD + lane * C;
+#pragma unroll
+  for (int i = 0; i < C; ++i) a[i] = f[i] = o[i];
+}
+
 template <int W>
 constexpr int kJoinWarps = W > 4 ? W : 4;   // of a block
 
@@ -1246,7 +1260,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>) join_kernel(const __grid_c
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (row >= p.B * p.Hq) return;
   const Entry e = p.entries[b];
-  if (e.lead < 0) return;
+  if (e.lead < 0) {                  // of no group: left as it was, but a step needs all rows
+    if (p.sink.out && sub == 0) {
+      if (lane == 0) report(p.status, MK_ERR_DEVICE, MK_OP_PREFIX_ATTENTION, b, -1, p.n_groups);
+      float zero[C] = {};
+      to_step<HD>(p, b, hq, zero);
+    }
+    return;
+  }
   const Line line(reinterpret_cast<const int*>(p.entries + p.B)[0], p.grid);
   float acc[C], m = -INFINITY, l = 0.0f;
 #pragma unroll
@@ -1346,9 +1367,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>) join_kernel(const __grid_c
   for (int i = 0; i < C; ++i) size += fabsf(acc[i]);
   if (__any_sync(kFull, !(size < INFINITY) || !(l < INFINITY))) row_alone<T, HD>(p, b, hq, e.group, acc, &m, &l);
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays
+#pragma unroll
+  for (int i = 0; i < C; ++i) acc[i] *= inv;
+  if (p.sink.out) {
+    to_step<HD>(p, b, hq, acc);
+    return;
+  }
   uint32_t o[C / 2];
 #pragma unroll
-  for (int i = 0; i < C; i += 2) o[i / 2] = Half<T>::pack(acc[i] * inv, acc[i + 1] * inv);
+  for (int i = 0; i < C; i += 2) o[i / 2] = Half<T>::pack(acc[i], acc[i + 1]);
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + (size_t)row * HD + lane * C);
 #pragma unroll
   for (int i = 0; i < C / 2; ++i) out[i] = o[i];
@@ -1461,32 +1488,28 @@ cudaError_t launch_attention(const AttnParams& p, const CUtensorMap* maps, int d
   return launch(join_kernel<T, HD, 1>, (rows + 3) / 4, 128, 0, st, p);
 }
 
-}  // namespace
-}  // namespace ops
-}  // namespace mk
-
-extern "C" size_t mk_prefix_attention_workspace(const mk_prefix_attention_args* a) {
-  using namespace mk::ops;
+size_t workspace_size(const mk_prefix_attention_args* a) {
   if (validate(a) != MK_OK) return 0;
   const size_t rows = part_rows(a);
   return round256(rows * a->head_dim * sizeof(float)) + round256(rows * sizeof(float2)) +
          round256(sizeof(Entry) * (size_t)a->batch + sizeof(int));
 }
 
-extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* a, void* stream) {
-  using namespace mk::ops;
+}  // namespace
+
+mk_status prefix_attention(const mk_prefix_attention_args* a, const StepSink& sink, cudaStream_t st) {
   mk_status s = validate(a);
   if (s != MK_OK) return s;
   if (a->batch == 0 || a->n_groups == 0) return MK_OK;
   if (!a->q || !a->k_pool || !a->v_pool || !a->page_table || !a->positions || !a->group_start ||
-      !a->prefix_lens || !a->out || !a->workspace)
+      !a->prefix_lens || !(a->out || sink.out) || !a->workspace)
     return MK_ERR_INVALID;
   const long long row = (long long)a->n_q_heads * a->head_dim;
   if (a->q_token_stride % 8 || (a->batch > 1 && a->q_token_stride < row)) return MK_ERR_INVALID;
   if (!aligned(a->q, 16) || !aligned(a->k_pool, 16) || !aligned(a->v_pool, 16) ||
       !aligned(a->out, 16) || !aligned(a->workspace, 256))
     return MK_ERR_INVALID;
-  if (a->workspace_bytes < mk_prefix_attention_workspace(a)) return MK_ERR_CAPACITY;
+  if (a->workspace_bytes < workspace_size(a)) return MK_ERR_CAPACITY;
   DeviceGuard guard(a->device);
   if (guard.status() != MK_OK) return guard.status();
   const int sms = sm_count(a->device);
@@ -1522,6 +1545,7 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* a, void
   p.n_slots = 2 * kMaxBlocks;
   p.out = a->out;
   p.lse = a->lse;
+  p.sink = sink;
   p.status = a->status;
 
   const auto type = a->type == MK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -1546,7 +1570,6 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* a, void
     box[2] = 1;
     if (!encode(&maps[3], type, 4, a->q, dims, strides, box)) return MK_ERR_INVALID;
   }
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a->type == MK_BF16)
     e = a->head_dim == 128 ? launch_attention<__nv_bfloat16, 128>(p, maps, a->device, st)
@@ -1555,4 +1578,15 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* a, void
     e = a->head_dim == 128 ? launch_attention<__half, 128>(p, maps, a->device, st)
                            : launch_attention<__half, 64>(p, maps, a->device, st);
   return from_cuda(e);
+}
+
+}  // namespace ops
+}  // namespace mk
+
+extern "C" size_t mk_prefix_attention_workspace(const mk_prefix_attention_args* args) {
+  return mk::ops::workspace_size(args);
+}
+
+extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* args, void* stream) {
+  return mk::ops::prefix_attention(args, mk::ops::StepSink{}, static_cast<cudaStream_t>(stream));
 }

@@ -30,6 +30,7 @@
 #include <cooperative_groups.h>
 
 #include "ops_common.cuh"
+#include "ops_step.h"
 
 namespace cg = cooperative_groups;
 
@@ -616,6 +617,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const int b = blockIdx.x / cluster;
   Cluster cl(&s, rank, cluster);
   cl.arrive();
+  // Nothing of the call's memory is touched before the kernels ahead are done.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   Row<T> row;
   row.id0 = rank * kThreads * p.per;
@@ -880,12 +884,14 @@ cudaError_t launch_sample(const SampleParams& p0, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)c;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, sample_kernel<T>, (const SampleParams)p, c);
 }
 

@@ -1,0 +1,23 @@
+// ops_step.cu -- what the decode step's form with shared prefixes needs on the
+// device besides the serving operators.
+#include "ops_step.h"
+
+namespace mk {
+namespace ops {
+namespace {
+
+__global__ void add_kernel(uint32_t* counters, const int32_t* pairs, int n) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < n) counters[pairs[2 * i]] += (uint32_t)pairs[2 * i + 1];
+}
+
+}  // namespace
+
+cudaError_t add_to_counters(uint32_t* counters, const int32_t* pairs, int n, cudaStream_t stream) {
+  if (n == 0) return cudaSuccess;
+  add_kernel<<<(n + 255) / 256, 256, 0, stream>>>(counters, pairs, n);
+  return cudaGetLastError();
+}
+
+}  // namespace ops
+}  // namespace mk

@@ -14,7 +14,7 @@ from typing import Dict, Optional, Sequence
 import numpy as np
 import torch
 
-from . import mk
+from . import mk, ops
 
 
 def _ptr(t: torch.Tensor) -> int:
@@ -56,6 +56,7 @@ class Decoder:
         t.w_down = arr(weights["w_down"])
         t.k_pool = arr([k_pool[l] for l in range(L)])
         t.v_pool = arr([v_pool[l] for l in range(L)])
+        self._inv_freq = None                       # of append_kv
         self._tensors = (weights, k_pool, v_pool)   # keep caller tensors alive
         ctx = c_void_p()
         mk.check_status(mk.lib.mk_create(byref(cfg), byref(t), int(device), byref(ctx)),
@@ -111,6 +112,98 @@ class Decoder:
                                      _ptr(page_table), _ptr(seq_lens), _ptr(logits),
                                      _ptr(out_tokens), c_void_p(s.cuda_stream))
         mk.check_status(st, "mk_decode_greedy")
+
+    def _groups(self, group_start: torch.Tensor, prefix_lens: torch.Tensor) -> int:
+        for t in (group_start, prefix_lens):
+            if t.dtype != torch.int32 or not t.is_cuda:
+                raise TypeError("group_start and prefix_lens must be int32 CUDA tensors")
+        n = prefix_lens.numel()
+        if not 1 <= n <= self.batch or group_start.numel() != n + 1:
+            raise ValueError("need 1 .. batch prefix lengths and one more group start")
+        return n
+
+    def step_shared(self, tokens: torch.Tensor, positions: torch.Tensor, page_table: torch.Tensor,
+                    seq_lens: torch.Tensor, group_start: torch.Tensor, prefix_lens: torch.Tensor,
+                    logits: torch.Tensor, stream=None) -> None:
+        """One step of a batch whose entries share prefixes (mk_decode_step_shared):
+        group g is entries group_start[g] .. group_start[g + 1] - 1, whose first
+        prefix_lens[g] tokens are read through the first entry's page-table row."""
+        for t in (tokens, positions, page_table, seq_lens):
+            if t.dtype != torch.int32 or not t.is_cuda:
+                raise TypeError("step inputs must be int32 CUDA tensors")
+        if logits.dtype != torch.float32 or not logits.is_cuda:
+            raise TypeError("logits must be a float32 CUDA tensor")
+        if page_table.shape[-1] != self.max_pages:
+            raise ValueError("page_table row length differs from the schedule's")
+        n = self._groups(group_start, prefix_lens)
+        s = stream if stream is not None else torch.cuda.current_stream()
+        st = mk.lib.mk_decode_step_shared(
+            self._ctx, _ptr(tokens), _ptr(positions), _ptr(page_table), _ptr(seq_lens), n,
+            _ptr(group_start), _ptr(prefix_lens), _ptr(logits), c_void_p(s.cuda_stream))
+        mk.check_status(st, "mk_decode_step_shared")
+
+    def sample(self, n_steps: int, tokens: torch.Tensor, positions: torch.Tensor,
+               page_table: torch.Tensor, seq_lens: torch.Tensor, logits: torch.Tensor,
+               out_tokens: torch.Tensor, u: torch.Tensor, *,
+               temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+               top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+               logprobs: Optional[torch.Tensor] = None,
+               group_start: Optional[torch.Tensor] = None,
+               prefix_lens: Optional[torch.Tensor] = None, stream=None) -> None:
+        """n_steps sampled steps on the device (mk_decode_sample): as ``greedy``,
+        with step i's tokens drawn by the uniform numbers u[i] under the rules of
+        ``ops.sample``; with group_start and prefix_lens the steps are those of
+        ``step_shared``.  logprobs, if given, receives n_steps x batch
+        log-probabilities.  Asynchronous."""
+        for t in (tokens, positions, page_table, seq_lens, out_tokens):
+            if t.dtype != torch.int32 or not t.is_cuda:
+                raise TypeError("sampling inputs and outputs must be int32 CUDA tensors")
+        if logits.dtype != torch.float32 or not logits.is_cuda:
+            raise TypeError("logits must be a float32 CUDA tensor")
+        if page_table.shape[-1] != self.max_pages:
+            raise ValueError("page_table row length differs from the schedule's")
+        if out_tokens.numel() < n_steps * self.batch:
+            raise ValueError("out_tokens holds fewer than n_steps x batch tokens")
+        how = mk.mk_sampling()
+        for name, t, dtype, size in (
+                ("u", u, torch.float32, n_steps * self.batch),
+                ("temperature", temperature, torch.float32, self.batch),
+                ("top_k", top_k, torch.int32, self.batch),
+                ("top_p", top_p, torch.float32, self.batch),
+                ("min_p", min_p, torch.float32, self.batch),
+                ("logprobs", logprobs, torch.float32, n_steps * self.batch)):
+            if t is None:
+                continue
+            if t.dtype != dtype or not t.is_cuda:
+                raise TypeError(f"{name} must be a {str(dtype)[6:]} CUDA tensor")
+            if t.numel() < size:
+                raise ValueError(f"{name} holds fewer than {size} values")
+            setattr(how, name, _ptr(t))
+        if (group_start is None) != (prefix_lens is None):
+            raise ValueError("group_start and prefix_lens go together")
+        if group_start is not None:
+            how.n_groups = self._groups(group_start, prefix_lens)
+            how.group_start, how.prefix_lens = _ptr(group_start), _ptr(prefix_lens)
+        s = stream if stream is not None else torch.cuda.current_stream()
+        st = mk.lib.mk_decode_sample(self._ctx, int(n_steps), _ptr(tokens), _ptr(positions),
+                                     _ptr(page_table), _ptr(seq_lens), _ptr(logits),
+                                     _ptr(out_tokens), byref(how), c_void_p(s.cuda_stream))
+        mk.check_status(st, "mk_decode_sample")
+
+    def append_kv(self, layer: int, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                  page_table: torch.Tensor, seq: Optional[torch.Tensor] = None,
+                  status: Optional["ops.Status"] = None, stream=None) -> None:
+        """Rotate a layer's keys and append them with their values to the cache
+        that the steps read (``ops.rope_append``): a prompt that was computed
+        outside the step, handed over in one piece.  k and v are [tokens][kv
+        heads][head size] before the rotation; the other arguments are
+        ``ops.rope_append``'s."""
+        _, k_pool, v_pool = self._tensors
+        if self._inv_freq is None:
+            self._inv_freq, _ = ops.rope_frequencies(
+                self.shape["head_dim"], self.shape.get("rope_theta", 1.0e4), device=k_pool.device)
+        ops.rope_append(None, k, v, positions, page_table, k_pool[layer], v_pool[layer],
+                        self._inv_freq, seq=seq, status=status, stream=stream)
 
     def check(self):
         """Synchronize and return (status, detail list)."""

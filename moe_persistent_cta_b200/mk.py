@@ -33,7 +33,8 @@ EXPORTS = (
     "mk_check", "mk_selftest_timeout", "mk_set_timeout_ms", "mk_set_trace", "mk_debug_read",
     "mk_debug_size",
     "mk_plan_schedule", "mk_rope_append", "mk_prefix_attention_workspace",
-    "mk_prefix_attention", "mk_sample", "mk_strerror", "mk_destroy",
+    "mk_prefix_attention", "mk_sample", "mk_decode_step_shared", "mk_decode_sample",
+    "mk_strerror", "mk_destroy",
 )
 
 
@@ -95,6 +96,11 @@ class mk_sample_args(ctypes.Structure):
                                 "logprobs", "status")]
 
 
+class mk_sampling(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("u", "temperature", "top_k", "top_p", "min_p", "logprobs",
+                                        "group_start", "prefix_lens")] + [("n_groups", c_int32)]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(
@@ -122,6 +128,9 @@ def _load():
         "mk_prefix_attention_workspace": (c_size_t, [c_void_p]),
         "mk_prefix_attention": (c_int, [c_void_p, c_void_p]),
         "mk_sample": (c_int, [c_void_p, c_void_p]),
+        "mk_decode_step_shared": (c_int, [c_void_p] + [c_void_p] * 4 + [c_int32] + [c_void_p] * 4),
+        "mk_decode_sample": (c_int, [c_void_p, c_int32] + [c_void_p] * 6 +
+                             [P(mk_sampling), c_void_p]),
         "mk_strerror": (c_char_p, [c_int]),
         "mk_destroy": (None, [c_void_p]),
     }

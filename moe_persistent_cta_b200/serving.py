@@ -164,10 +164,78 @@ def fill_prefix_kv(k_pool: torch.Tensor, v_pool: torch.Tensor, pages: List[int],
                                                   device=k_pool.device).to(torch.bfloat16))
 
 
+def sampling_rules(sampling: Dict, rows: int, device) -> Dict[str, torch.Tensor]:
+    """The per-row tensors of ``Decoder.sample`` from one value for all rows."""
+    kinds = {"temperature": torch.float32, "top_k": torch.int32, "top_p": torch.float32,
+             "min_p": torch.float32}
+    unknown = set(sampling) - set(kinds)
+    if unknown:
+        raise ValueError(f"unknown sampling rules {sorted(unknown)}")
+    return {name: torch.full((rows,), sampling[name], dtype=kinds[name], device=device)
+            for name in sampling}
+
+
+def sample_prompt(dec, k_pool: torch.Tensor, v_pool: torch.Tensor, pool: PagePool,
+                  prompt_pages: List[int], prompt_len: int, tokens: List[int], steps: int, *,
+                  max_pages_per_seq: int, seed: int = 0, sampling: Optional[Dict] = None,
+                  stream=None) -> Dict:
+    """Several samples of one cached prompt: sample i feeds tokens[i] and then
+    ``steps`` drawn tokens, reading the prompt's whole pages through one page
+    list, once per step for all samples (mk_decode_step_shared).
+
+    The prompt's ``prompt_len`` tokens lie in ``prompt_pages`` of every layer's
+    pools.  Where it ends inside a page, that page is copied for each sample;
+    the pages of the samples come from ``pool`` and go back before the return.
+    The schedule must be built for len(tokens) entries.  Returns the drawn tokens
+    and their log-probabilities, [steps][samples], and the last logits."""
+    dev = k_pool.device
+    n = len(tokens)
+    whole, rest = divmod(prompt_len, PAGE)
+    if len(prompt_pages) < pages_for(prompt_len):
+        raise ValueError("prompt_pages does not hold prompt_len tokens")
+    need = pages_for(prompt_len + steps)
+    if need > max_pages_per_seq:
+        raise ValueError("the samples outgrow the page table")
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    own: List[List[int]] = []
+    try:
+        for _ in range(n):
+            own.append(pool.alloc(need - whole))
+        table = np.full((n, max_pages_per_seq), -1, dtype=np.int32)
+        for i in range(n):
+            table[i, :whole] = prompt_pages[:whole]
+            table[i, whole:need] = own[i]
+        i32 = dict(dtype=torch.int32, device=dev)
+        with torch.cuda.stream(s):
+            if rest:
+                last = prompt_pages[whole]
+                for i in range(n):
+                    for p in (k_pool, v_pool):
+                        p[:, own[i][0]] = p[:, last]
+            toks = torch.tensor(tokens, **i32)
+            lens = torch.full((n,), prompt_len, **i32)
+            table_d = torch.from_numpy(table).to(dev)
+            out = torch.full((steps, n), -1, **i32)
+            logprobs = torch.zeros((steps, n), dtype=torch.float32, device=dev)
+            logits = torch.empty((n, dec.shape["vocab"]), dtype=torch.float32, device=dev)
+            u = torch.rand((steps, n), device=dev,
+                           generator=torch.Generator(device=dev).manual_seed(seed))
+            dec.sample(steps, toks, lens, table_d, lens, logits, out, u, logprobs=logprobs,
+                       group_start=torch.tensor([0, n], **i32),
+                       prefix_lens=torch.tensor([whole * PAGE], **i32), stream=s,
+                       **sampling_rules(sampling or {}, n, dev))
+        s.synchronize()
+        dec.check_ok()
+    finally:
+        for pages in own:
+            pool.release(pages)
+    return {"tokens": out.cpu().numpy(), "logprobs": logprobs.cpu().numpy(), "logits": logits}
+
+
 def run_continuous(dec, shape: Dict, k_pool: torch.Tensor, v_pool: torch.Tensor, slots: int,
                    steps: int, seed: int, start_lo: int, start_hi: int, mean_new: float,
                    max_new: int, max_pages_per_seq: int, stream=None,
-                   horizon: Optional[int] = None) -> Dict:
+                   horizon: Optional[int] = None, sampling: Optional[Dict] = None) -> Dict:
     """Run `steps` greedy decode steps with slot refills.
 
     A sequence's stop length is drawn when it starts, so the host knows when
@@ -177,8 +245,10 @@ def run_continuous(dec, shape: Dict, k_pool: torch.Tensor, v_pool: torch.Tensor,
     (page pool, synthetic prefix, token and length written to the device
     buffers on the same stream) and goes on.  Times are taken with CUDA
     events on the stream: the greedy steps (decode_s), the synthetic prefix
-    fills (prefix_fill_s) and schedule rebuilds (rebuild_s, host).  Returns
-    counts, times, the generated tokens [steps][slots] and the cached length
+    fills (prefix_fill_s) and schedule rebuilds (rebuild_s, host).  With
+    ``sampling``, a dict of temperature, top_k, top_p and min_p (each optional,
+    for all slots alike), tokens are drawn on the device (mk_decode_sample) from
+    seeded uniform numbers instead.  Returns counts, times, the generated tokens [steps][slots] and the cached length
     of every slot at every step (for the KV bytes the steps read)."""
     dev = k_pool.device
     rng = np.random.default_rng(seed)
@@ -193,6 +263,8 @@ def run_continuous(dec, shape: Dict, k_pool: torch.Tensor, v_pool: torch.Tensor,
     table_d = torch.zeros((slots, max_pages_per_seq), **i32)
     out = torch.full((steps, slots), -1, **i32)
     logits = torch.empty((slots, shape["vocab"]), dtype=torch.float32, device=dev)
+    rules = sampling_rules(sampling, slots, dev) if sampling is not None else None
+    gen_u = torch.Generator(device=dev).manual_seed(seed + 1)
     ev = []            # (kind, start event, end event)
     t_rebuild = 0.0
     rebuilds = 0
@@ -237,7 +309,12 @@ def run_continuous(dec, shape: Dict, k_pool: torch.Tensor, v_pool: torch.Tensor,
                 lens_per_step[done + j] = [q.cached + j for q in sched.seqs]
             e0 = torch.cuda.Event(enable_timing=True)
             e0.record(s)
-            dec.greedy(n, tokens, lens_d, table_d, lens_d, logits, out[done:done + n], stream=s)
+            if rules is None:
+                dec.greedy(n, tokens, lens_d, table_d, lens_d, logits, out[done:done + n], stream=s)
+            else:
+                u = torch.rand((n, slots), generator=gen_u, device=dev)
+                dec.sample(n, tokens, lens_d, table_d, lens_d, logits, out[done:done + n], u,
+                           stream=s, **rules)
             e1 = torch.cuda.Event(enable_timing=True)
             e1.record(s)
             ev.append(("decode", e0, e1))

@@ -173,3 +173,20 @@ def test_oracle_attention_is_softmax_over_the_pages():
     want = torch.softmax(q[1] @ k.T * 0.125, -1) @ v
     assert torch.allclose(out[1], want)
     assert torch.allclose(lse[1], torch.logsumexp(q[1] @ k.T * 0.125, -1))
+
+
+def test_decode_loop_refusals_without_a_context():
+    how = mk.mk_sampling()
+    assert mk.lib.mk_decode_step_shared(None, P, P, P, P, 1, P, P, P, None) == mk.MK_ERR_INVALID
+    assert mk.lib.mk_decode_sample(None, 1, P, P, P, P, P, P, byref(how), None) == mk.MK_ERR_INVALID
+    # the struct as the C compiler lays it out: eight pointers and a count
+    assert ctypes.sizeof(mk.mk_sampling) == 8 * 8 + 8
+
+
+def test_sampling_rules():
+    from moe_persistent_cta_b200 import serving
+    r = serving.sampling_rules(dict(temperature=0.5, top_k=7), 3, "cpu")
+    assert r["temperature"].tolist() == [0.5] * 3 and r["top_k"].tolist() == [7] * 3
+    assert r["top_k"].dtype == torch.int32 and set(r) == {"temperature", "top_k"}
+    with pytest.raises(ValueError):
+        serving.sampling_rules(dict(top_q=0.5), 3, "cpu")
