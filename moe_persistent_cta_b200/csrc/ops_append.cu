@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
   };
   // Nothing of the call's memory is touched before the kernels ahead are done.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (t >= p.T) return;
   const int pos = __ldg(p.positions + t), seq = p.seq ? __ldg(p.seq + t) : t;
   Raw<S> raw[kAhead];

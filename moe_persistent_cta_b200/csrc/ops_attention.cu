@@ -722,7 +722,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // Nothing of the call's memory is touched before the kernels ahead are done.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Barrier use counts, carried from pass to pass by every role that needs them.
   // (No arrays: one whose index is not known when compiling would lie in memory,
@@ -1257,7 +1256,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>) join_kernel(const __grid_c
   const int row = (int)blockIdx.x * (kJoinWarps<W> / W) + warp / W;
   const int b = row / p.Hq, hq = row % p.Hq, h = hq / p.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (row >= p.B * p.Hq) return;
   const Entry e = p.entries[b];
   if (e.lead < 0) {                  // of no group: left as it was, but a step needs all rows
@@ -1447,7 +1445,9 @@ mk_status validate(const mk_prefix_attention_args* a) {
 }
 
 // Both launches may begin while the one ahead is finishing: they wait for it
-// before they touch memory.
+// before they touch memory.  Neither lets the one behind begin earlier than its
+// own blocks end: that one's blocks would take the room that the join's are
+// waiting for (256 entries on 32768 tokens: 149 us, not 135).
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t st,
                    const A&... args) {

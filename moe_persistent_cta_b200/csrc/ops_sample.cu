@@ -12,7 +12,7 @@
 // neighbour of the defined token in a few per cent of the rows.  All sums are
 // taken in a fixed order, so a call gives the same tokens every time.
 //
-// Bound: one read of the logits.  A cluster of up to 8 blocks holds a row in
+// Bound: one read of the logits.  A cluster of up to 8 (few rows: 16) blocks holds a row in
 // its shared memory, so the passes below touch memory once.  The cut is found
 // by one of three ways:
 //  * top_k up to 512: the k-th largest of the maxima of 512 groups of tokens is a
@@ -29,6 +29,8 @@
 // by a bitonic sort).
 #include <cooperative_groups.h>
 
+#include <mutex>
+
 #include "ops_common.cuh"
 #include "ops_step.h"
 
@@ -40,7 +42,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kCluster = 8;          // blocks of a row, at most ...
+constexpr int kMaxCluster = 16;      // ... and where so many clusters run at once anyway
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kList = 2 * kThreads;  // tokens that can be gathered and ordered
 constexpr int kBins = kWarps;        // parts of a range of logits, one per warp
@@ -100,11 +103,11 @@ struct Shared {
         double w[kThreads];
         int id[kThreads], by_id[kThreads];
       } draw;                              // the draw among sorted tokens
+      uint32_t group_max[kThreads];
     };
     float bins[kBins][kThreads];           // sums of weights, each thread its own
   };
   double exp2_tab[256];              // 2^(j / 256)
-  uint32_t group_max[kThreads];
   double warp_val[kWarps][3];
   unsigned long long warp_key[kWarps];
   Exchange ex;
@@ -529,11 +532,12 @@ __device__ bool draw_sorted(Shared* s, const Row<T>& row, int keep, float min_p,
   return true;
 }
 
-// The cut of top_p over all tokens, by narrowing.  False if it has to be found
+// The cut of top_p over all tokens, by narrowing; also this thread's sum of the
+// tokens nearer to the largest than *from, all of which are kept.  False if it has to be found
 // another way (the same in every thread of the cluster).
 template <typename T>
 __device__ bool narrow_cut(Cluster& cl, Shared* s, const Row<T>& row, int V, float top_p, float temp,
-                           uint32_t* cut, uint32_t* cut_id) {
+                           uint32_t* cut, uint32_t* cut_id, float* from_out, double* above_out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double sum = 0.0, t[3];
   weigh(row, [](float, int) { return true; }, [&](int, double w) { sum += w; });
@@ -606,6 +610,8 @@ __device__ bool narrow_cut(Cluster& cl, Shared* s, const Row<T>& row, int V, flo
   if (s->cut == 0) return false;
   *cut = s->cut;
   *cut_id = s->cut_id;
+  *from_out = from;
+  *above_out = above;
   return true;
 }
 
@@ -619,7 +625,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   cl.arrive();
   // Nothing of the call's memory is touched before the kernels ahead are done.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (No early word to the kernel behind: its blocks would take room from this
+  // one's: 33 rows of 151541, 29 us and not 24.)
 
   Row<T> row;
   row.id0 = rank * kThreads * p.per;
@@ -718,6 +725,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     uint32_t cut = floor_key, cut_id = 0xffffffffu;
     bool settled = false;            // block 0 has drawn among the gathered tokens
     double t[3];
+    float from = -INFINITY;          // this thread's tokens nearer than this are in `summed`
+    double summed = 0.0;
     const bool limited = k > 0 && k < p.V;
     if (limited && k <= kThreads) {
       // the k-th largest of the groups' maxima to 20 bits, rounded down: k
@@ -751,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const uint32_t key = key_of(x);
         return key > cut || (key == cut && (uint32_t)id <= cut_id);
       };
-      if (top_p < 1.0f && (limited || row.inf || !narrow_cut(cl, &s, row, p.V, top_p, temp, &cut, &cut_id))) {
+      if (top_p < 1.0f && (limited || row.inf || !narrow_cut(cl, &s, row, p.V, top_p, temp, &cut, &cut_id, &from, &summed))) {
         double sum = 0.0;
         weigh(row, kept, [&](int, double w) { sum += w; });
         cl.sum3(sum, 0.0, 0.0, t);
@@ -789,10 +798,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       // the draw, in id order
       double mine = 0.0;
       int last = -1;
-      weigh(row, kept, [&](int i, double w) {
+      if (min_p > 0.0f) from = -INFINITY;    // not all of those are kept
+      if (from > -INFINITY) {
+        mine = summed;
+        each(row, [&](float x, int i) {
+          if (row.mx - x < from) last = i;
+        });
+      }
+      weigh(row, [&](float x, int id) { return !(row.mx - x < from) && kept(x, id); }, [&](int i, double w) {
         if (w < (double)min_p || w == 0.0) return;
         mine += w;
-        last = i;
+        last = max(last, i);
       });
       double under[3];
       const bool here = cl.sum_drawn(mine, u, t, under);
@@ -856,40 +872,86 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   // No barrier: behind the last one no block touches another's memory.
 }
 
-// Blocks a row is spread over and consecutive tokens of a thread.  The part a
-// thread walks is an odd number of elements, so that the 32 threads of a warp
-// read 32 banks.
-int cluster_for(int vocab) {
-  int c = 1;
-  while (c < kMaxCluster && vocab > c * kThreads * 4) c *= 2;
-  return c;
+constexpr size_t smem_for(int per, size_t size) { return (size_t)per * kThreads * size + 16; }
+// Consecutive tokens of a thread: an odd number, so that the 32 threads of a
+// warp read 32 banks.
+constexpr int per_thread(int vocab, int cluster) {
+  return ((vocab + cluster * kThreads - 1) / (cluster * kThreads)) | 1;
+}
+static_assert(smem_for(per_thread(MK_SAMPLE_MAX_VOCAB, kCluster), 4) + sizeof(Shared) <= 227 * 1024,
+              "the largest vocabulary does not fit the cluster's shared memory");
+
+// What a device allows the kernel, asked once: shared memory, clusters of 16
+// blocks, and how many of those run at the same time, with one block on a
+// multiprocessor and with two.
+struct Allowed {
+  std::once_flag once;
+  cudaError_t error = cudaSuccess;
+  int wide[2] = {0, 0};
+};
+constexpr size_t kHalfDevice = 113 * 1024;   // shared memory of a block, where two run
+constexpr int kMaxDevices = 64;
+
+template <typename T>
+const Allowed& allowed(int device) {
+  static Allowed all[kMaxDevices];
+  Allowed& a = all[device];
+  std::call_once(a.once, [&] {
+    auto kernel = sample_kernel<T>;
+    constexpr int most = (int)smem_for(per_thread(MK_SAMPLE_MAX_VOCAB, kCluster), sizeof(T));
+    a.error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (a.error != cudaSuccess) return;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kMaxCluster);
+    cfg.blockDim = dim3(kThreads);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kMaxCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    for (int two = 0; two < 2; ++two) {
+      cfg.dynamicSmemBytes = two ? kHalfDevice - sizeof(Shared) : (size_t)most;
+      if (cudaOccupancyMaxActiveClusters(&a.wide[two], kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        a.wide[two] = 0;
+      }
+    }
+  });
+  return a;
 }
 
 template <typename T>
-cudaError_t launch_sample(const SampleParams& p0, cudaStream_t stream) {
+cudaError_t launch_sample(const SampleParams& p0, int device, cudaStream_t stream) {
+  if (device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
+  const Allowed& a = allowed<T>(device);
+  if (a.error != cudaSuccess) return a.error;
   SampleParams p = p0;
-  const int c = cluster_for(p.V);
-  p.per = ((p.V + c * kThreads - 1) / (c * kThreads)) | 1;
-  const size_t smem = (size_t)p.per * kThreads * sizeof(T) + 16;
-  static_assert((MK_SAMPLE_MAX_VOCAB / (kMaxCluster * kThreads) + 1) * kThreads * 4 + 16 +
-                        sizeof(Shared) <= 227 * 1024,
-                "the largest vocabulary does not fit the cluster's shared memory");
-  cudaError_t e = cudaSuccess;
-  if (smem > 8 * 1024)               // with Shared more than the default 48 KB
-    e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
-  if (e != cudaSuccess) return e;
+  // Blocks of a row: four tokens a thread at least; 16 where all rows then still
+  // run at once (7 on B200; 4 rows of 151552 with top_p: 30.6 us, with 8 blocks
+  // 39.8; with 8 rows one would wait for the others).
+  int c = 1;
+  while (c < kCluster && p.V > c * kThreads * 4) c *= 2;
+  if (c == kCluster && p.V > c * kThreads * 4) {
+    const size_t block = smem_for(per_thread(p.V, kMaxCluster), sizeof(T)) + sizeof(Shared);
+    if (p.B <= a.wide[block <= kHalfDevice]) c = kMaxCluster;
+  }
+  p.per = per_thread(p.V, c);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(p.B * c));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = smem_for(p.per, sizeof(T));
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)c;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, sample_kernel<T>, (const SampleParams)p, c);
@@ -924,9 +986,9 @@ mk_status sample(const mk_sample_args* a, int32_t* next_token, int32_t* position
   p.next_token = next_token;
   p.position = position;
   p.seq_len = seq_len;
-  if (a->type == MK_FP32) return from_cuda(launch_sample<float>(p, stream));
-  if (a->type == MK_BF16) return from_cuda(launch_sample<__nv_bfloat16>(p, stream));
-  return from_cuda(launch_sample<__half>(p, stream));
+  if (a->type == MK_FP32) return from_cuda(launch_sample<float>(p, a->device, stream));
+  if (a->type == MK_BF16) return from_cuda(launch_sample<__nv_bfloat16>(p, a->device, stream));
+  return from_cuda(launch_sample<__half>(p, a->device, stream));
 }
 
 }  // namespace ops

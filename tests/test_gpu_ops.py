@@ -490,3 +490,173 @@ def test_sample_same_result_every_time():
     for _ in range(20):
         again = ops.sample(x, u, top_p=p, top_k=k, logprobs=lp)
         assert torch.equal(first, again) and torch.equal(lp0, lp)
+
+
+# --------------------------------------------- calls at the edge of the rules --
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_attention_values_of_other_entries_do_not_leak(hd, dt):
+    """Infinities and NaN that one entry sees stay with it: in its own tokens,
+    whose tiles share rows with other entries, and in prefix tokens that a
+    shorter member of the group does not reach."""
+    g = gen(31)
+    n, prefix, hkv, hq = 5, 192, 2, 4
+    positions = [250, 300, 100, 199, 260]                # entry 2 ends inside the prefix
+    width = 5
+    table = torch.full((n, width), 0, dtype=torch.int32)
+    nxt = 3
+    for i in range(n):
+        table[i, :3] = torch.arange(3)
+        for page in range(3, width):
+            table[i, page] = nxt
+            nxt += 1
+    kp, vp = (torch.randn((nxt, hkv, PAGE, hd), generator=g).to(TYPES[dt]) for _ in range(2))
+    q = torch.randn((n, hq, hd), generator=g).to(TYPES[dt])
+    clean = ops_oracle.attention(q, kp, vp, table, positions, [0, n], [prefix], hd ** -0.5)
+    vp[int(table[0, 3]), 0, 5] = math.inf                # entry 0 sees it, in KV head 0
+    kp[int(table[1, 4]), 1, 3] = math.nan                # entry 1 sees it, in KV head 1
+    vp[2, 1, 10] = -math.inf                             # prefix token 138: all but entry 2 see it
+    out = torch.full((n, hq, hd), 9.0, dtype=TYPES[dt], device=DEV)
+    lse = torch.full((n, hq), 9.0, device=DEV)
+    ops.prefix_attention(q.to(DEV), kp.to(DEV), vp.to(DEV), table.to(DEV), i32(positions), i32([0, n]),
+                         i32([prefix]), out=out, lse=lse)
+    got = out.cpu().float()
+    assert not torch.isfinite(got[0, :2]).any()          # its own infinity
+    assert torch.isnan(got[1, 2:]).all() and torch.isnan(lse.cpu()[1, 2:]).all()
+    for b in (0, 1, 3, 4):
+        assert not torch.isfinite(got[b, 2:]).any()      # the prefix's, in KV head 1
+    # the others are as if nothing were there
+    for b, heads in ((1, slice(0, 2)), (2, slice(0, 4)), (3, slice(0, 2)), (4, slice(0, 2))):
+        o, s, mass, high = (x[b, heads] for x in clean)
+        h = torch.finfo(TYPES[dt]).eps / 2
+        tol = h * (mass + o.abs()) + (2e-5 * (1.0 + high))[..., None] * mass + 1e-7
+        assert ((got[b, heads].double() - o).abs() <= tol).all()
+        assert ((lse.cpu()[b, heads].double() - s).abs() <= 2e-5 * (1.0 + high)).all()
+
+
+def test_attention_full_rows_and_largest_batch():
+    # the last token of a row that has no page to spare
+    attention_case(32, [2], [128], [191, 150], 4, 2, 64, "bf16")
+    g = gen(33)
+    kp, vp = (torch.randn((6, 2, PAGE, 64), generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((2, 4, 64), generator=g).to(torch.bfloat16)
+    table = torch.tensor([[4, 0, 2], [1, 5, 3]], dtype=torch.int32)
+    out, lse = torch.full((2, 4, 64), 9.0, dtype=torch.bfloat16, device=DEV), torch.full((2, 4), 9.0, device=DEV)
+    status = ops.Status(DEV)
+    ops.prefix_attention(q.to(DEV), kp.to(DEV), vp.to(DEV), table.to(DEV), i32([191, 191]), i32([0, 2]), i32([100]),
+                         out=out, lse=lse, status=status)
+    status.check_ok()
+    # tokens behind the prefix come from the entry's own row
+    check_attention(out, lse, ops_oracle.attention(q, kp, vp, table, [191, 191], [0, 2], [100], 0.125), "bf16")
+    n = 4096
+    attention_case(34, [1] * n, [0] * n, [(i * 7) % 5 for i in range(n)], 1, 1, 64, "bf16")
+    attention_case(35, [40] + [0] * 4000 + [3], [70] + [0] * 4000 + [5], [70 + i for i in range(40)] + [5, 4, 9],
+                   8, 2, 64, "bf16")
+
+
+@pytest.mark.parametrize("members,prefix", [(3, 0), (40, 130), (70, 200)])
+def test_attention_many_heads_over_many_blocks(members, prefix):
+    # one KV head per query head and eight of them: chunks of entries at every place of the line
+    attention_case(members + prefix, [members, 2], [prefix, 64],
+                   [prefix + (i * 37) % 300 for i in range(members)] + [64, 400], 16, 8, 64, "fp16")
+
+
+def test_a_step_of_all_three_captured_and_replayed():
+    """Append, attend and sample as a decode loop would, captured twice on a side
+    stream (two graphs alive at once) and replayed in turn with other inputs."""
+    hq, hkv, hd, b, vocab = 4, 2, 64, 3, 500
+    freq, _ = ops.rope_frequencies(hd, device=DEV)
+    table = i32([[0, 1], [2, 3], [4, 5]])
+    proj = torch.randn((vocab, hq * hd), generator=gen(50)).to(DEV)
+
+    def state(seed):
+        g = gen(seed)
+        s = dict(qkv=torch.randn((b, hq + 2 * hkv, hd), generator=g).to(DEV),
+                 kp=torch.randn((6, hkv, PAGE, hd), generator=g).to(torch.bfloat16).to(DEV),
+                 vp=torch.randn((6, hkv, PAGE, hd), generator=g).to(torch.bfloat16).to(DEV),
+                 pos=i32([70, 5, 127]), u=torch.rand(b, generator=g).to(DEV), tokens=i32([-9] * b),
+                 out=torch.zeros((b, hq, hd), dtype=torch.bfloat16, device=DEV))
+        s["q"] = torch.zeros_like(s["out"])
+        return s
+
+    def step(s):
+        ops.rope_append(s["qkv"][:, :hq], s["qkv"][:, hq:hq + hkv], s["qkv"][:, hq + hkv:], s["pos"], table, s["kp"],
+                        s["vp"], freq, q_out=s["q"])
+        ops.prefix_attention(s["q"], s["kp"], s["vp"], table, s["pos"], i32_start, i32_prefix, out=s["out"])
+        logits = s["out"].view(b, -1).float() @ proj.t()
+        ops.sample(logits, s["u"], tokens=s["tokens"], top_k=topk)
+        return logits
+
+    i32_start, i32_prefix, topk = i32([0, 1, 2, 3]), i32([0, 0, 0]), i32([50] * b)
+    graphs = []
+    for seed in (41, 42):
+        s = state(seed)
+        step(s)
+        torch.cuda.synchronize()
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            logits = step(s)
+        graphs.append((graph, s, logits))
+    for turn in range(3):
+        for n, (graph, s, logits) in enumerate(graphs):
+            fresh = state(100 + 10 * turn + n)
+            for k in ("qkv", "kp", "vp", "u"):
+                s[k].copy_(fresh[k])
+            s["pos"].copy_(i32([turn, 64 + turn, 100 - turn]))
+            fresh["pos"].copy_(s["pos"])
+            graph.replay()
+            want = step(fresh)
+            torch.cuda.synchronize()
+            for k in ("kp", "vp", "q", "out", "tokens"):
+                assert torch.equal(s[k], fresh[k]), (turn, n, k)
+            assert torch.equal(logits, want)
+
+
+def test_streams_are_waited_for():
+    """Each operator on a side stream, behind work of that stream that makes its
+    inputs: launches overlap the kernel ahead but not its results."""
+    side = torch.cuda.Stream()
+    freq, _ = ops.rope_frequencies(64, device=DEV)
+    big = torch.randn((4096, 4096), device=DEV)
+    k_src = torch.randn((40, 1, 64), device=DEV)
+    table = i32([[0]])
+    positions, seq = torch.arange(40, dtype=torch.int32, device=DEV), torch.zeros(40, dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    results = []
+    for stream in (None, side):
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            k = torch.zeros_like(k_src)
+            kp, vp = (torch.zeros((1, 1, PAGE, 64), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+            for _ in range(3):
+                big @ big
+            k.copy_(k_src)
+            q = ops.rope_append(k, k, k, positions, table, kp, vp, freq, seq=seq, stream=stream)
+            o = ops.prefix_attention(q[39:], kp, vp, table, positions[39:], seq[:2].clone() + i32([0, 1]),
+                                     seq[:1], stream=stream)
+            t = ops.sample(o.view(1, -1), torch.full((1,), 0.5, device=DEV), stream=stream)
+        torch.cuda.synchronize()
+        results.append((q, kp, vp, o, t))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_sample_small_batches_and_wide_rows():
+    # rows spread over the most blocks, and those that just are not
+    r = np.random.default_rng(14)
+    for b, v in ((1, 151552), (2, 16384), (2, 16385), (7, 40000), (8, 40000), (1, mk.MK_SAMPLE_MAX_VOCAB)):
+        x = 2.5 * r.standard_normal((b, v))
+        sample_case(x, r.random(b))
+        sample_case(x, r.random(b), p=[0.9] * b)
+        sample_case(x, r.random(b), k=[300] * b, p=[0.95] * b)
+        sample_case(x, r.random(b), k=[700] * b)
+        sample_case(x, r.random(b), p=[0.95] * b, m=[0.01] * b, temperature=[1.5] * b)
+
+
+def test_sample_top_p_where_the_weights_lie_flat():
+    # the cut among thousands of nearly equal logits, at every level of narrowing
+    r = np.random.default_rng(15)
+    x = np.concatenate((1e-3 * r.standard_normal((4, 30000)), 1e-6 * r.standard_normal((4, 30000)) + 0.5), axis=1)
+    for p in (0.05, 0.3, 0.62, 0.9, 0.999):
+        sample_case(x, r.random(4), p=[p] * 4)
+    sample_case(x.astype(np.float16), r.random(4), p=[0.6] * 4, dt="fp16")
