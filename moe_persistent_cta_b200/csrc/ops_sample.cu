@@ -687,6 +687,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (threadIdx.x < 256) s.exp2_tab[threadIdx.x] = exp2((double)threadIdx.x / 256.0);
   {
     uint32_t g = top;
+    if (vecs < kThreads) {           // some threads have loaded nothing: go by the tokens they walk
+      __syncthreads();
+      g = 0;
+      for (int i = row.lo; i < row.hi; ++i) g = max(g, key_of(to_float(vals[i])));
+    }
 #pragma unroll
     for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
       const uint32_t other = __shfl_xor_sync(kFull, g, o);

@@ -12,6 +12,7 @@ streams may overlap it as long as they write other tensors.
 
 from __future__ import annotations
 
+import functools
 import math
 import struct
 from typing import Optional
@@ -71,6 +72,13 @@ def _cuda(t: torch.Tensor, name: str) -> int:
     if dev < 0 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     return dev
+
+
+@functools.lru_cache(maxsize=None)
+def _workspace_size(batch: int, hq: int, hkv: int, hd: int) -> int:
+    """mk_prefix_attention_workspace, which goes by these sizes alone."""
+    return mk.lib.mk_prefix_attention_workspace(_PACK_ATTENTION(
+        0, batch, 1, 1, 1, hq, hkv, hd, mk.MK_BF16, 1.0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0))
 
 
 def _stream(stream, dev: int) -> int:
@@ -253,24 +261,25 @@ def prefix_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
           or out.get_device() != dev):
         raise ValueError("out must be contiguous with q's shape, type and device")
     handle = _stream(stream, dev)
-    args = (dev, b, n, pages, n_pages, hq, hkv, hd, _TYPE[dtype],
+    if b == 0 or n == 0:
+        return out
+    # the workspace is this call's own; torch hands its memory on in stream order
+    size = _workspace_size(b, hq, hkv, hd)
+    if stream is None:
+        work = q.new_empty(size, dtype=torch.uint8)
+    else:
+        with torch.cuda.stream(stream):
+            work = q.new_empty(size, dtype=torch.uint8)
+    a = _PACK_ATTENTION(
+            dev, b, n, pages, n_pages, hq, hkv, hd, _TYPE[dtype],
             1.0 / math.sqrt(hd) if scale is None else scale, q.data_ptr(), qs[0], k_pool.data_ptr(),
             v_pool.data_ptr(), _array(page_table, _I32, "page_table", dev, (b, pages)),
             _array(positions, _I32, "positions", dev, (b,)),
             _array(group_start, _I32, "group_start", dev, (n + 1,)),
             _array(prefix_lens, _I32, "prefix_lens", dev, (n,)), out.data_ptr(),
-            0 if lse is None else _array(lse, _F32, "lse", dev, (b, hq)))
-    st = _status(status, dev)
-    if b == 0 or n == 0:
-        return out
-    size = mk.lib.mk_prefix_attention_workspace(_PACK_ATTENTION(*args, 0, 0, st))
-    # the workspace is this call's own; torch hands its memory on in stream order
-    if stream is None:
-        work = torch.empty(size, dtype=torch.uint8, device=q.device)
-    else:
-        with torch.cuda.stream(stream):
-            work = torch.empty(size, dtype=torch.uint8, device=q.device)
-    rc = mk.lib.mk_prefix_attention(_PACK_ATTENTION(*args, work.data_ptr(), size, st), handle)
+            0 if lse is None else _array(lse, _F32, "lse", dev, (b, hq)), work.data_ptr(), size,
+            _status(status, dev))
+    rc = mk.lib.mk_prefix_attention(a, handle)
     if rc:
         raise mk.MKError(rc, "mk_prefix_attention")
     return out
