@@ -290,6 +290,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : MK_W16(r, 0), MK_W16(r, 16)::"memory");
 }
+__device__ __forceinline__ void tmem_wait_ld64(uint32_t* r) {
+  tmem_wait_ld32(r);
+  asm volatile("" : MK_W16(r, 32), MK_W16(r, 48)::"memory");
+}
 #undef MK_W4
 #undef MK_W16
 __device__ __forceinline__ void tmem_wait_st() {
@@ -308,9 +312,9 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t lead_bytes) 
 struct Bars {
   uint64_t full[10], empty[10];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_ready[4];    // p_ready: two halves of a tile's tokens per stream
+  uint64_t s_full[4], p_ready[4];    // per stream, of the two halves of a tile's tokens
+  uint64_t pv_done[2];               // P V of the first half of a stream's last step
   uint64_t o_full[2], o_free[2];
-  uint64_t turn[2];                  // the other stream has taken its exponentials
 };
 
 struct Block {
@@ -354,6 +358,7 @@ struct Walk {
   int n, base;                       // items, unit of the first
   int i = 0, j = 0, run = 0;         // item, step of it, run
   int count = 0, j0 = 0, total = 0;  // the item's steps, those of the run before it and in all
+  int tile = 0, tile1 = -1, tile2 = -1;   // number of the step's tile, of those one and two steps before
   bool dual = false;
   __device__ __forceinline__ Walk(const Item* it, int n_items, int first) : items(it), n(n_items), base(first) {
     enter();
@@ -367,6 +372,11 @@ struct Walk {
     total = q.steps;
   }
   __device__ __forceinline__ const Item& at() const { return items[(base + i) % kMaxItems]; }
+  __device__ __forceinline__ bool done() const { return i >= n; }
+  // Places in the ring of a step that loads: K lies behind the V tiles of the
+  // steps up to the last but one, V behind the K tiles up to the next step's.
+  __device__ __forceinline__ uint32_t k_place() const { return tile + tile2 + 1; }
+  __device__ __forceinline__ uint32_t v_place(bool another) const { return 2 * tile + 1 + (!dual && another ? 1 : 0); }
   __device__ __forceinline__ bool loads() const { return !(dual && (j & 1)); }   // a new tile
   __device__ __forceinline__ bool first() const { return j0 + j == 0; }          // of the run
   __device__ __forceinline__ bool last() const { return j0 + j == total - 1; }
@@ -375,10 +385,15 @@ struct Walk {
   __device__ __forceinline__ int q_slot(int stream) const { return dual ? stream : (run & 1); }
   __device__ __forceinline__ void next() {
     if (last()) ++run;
+    tile2 = tile1;
+    tile1 = tile;
     if (++j == count) {
       j = 0;
       ++i;
       enter();
+      ++tile;
+    } else if (loads()) {
+      ++tile;
     }
   }
 };
@@ -687,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t b_full = saddr(s.bars.full), b_empty = saddr(s.bars.empty);
   const uint32_t b_qfull = saddr(s.bars.q_full), b_qempty = saddr(s.bars.q_empty);
   const uint32_t b_sfull = saddr(s.bars.s_full), b_pready = saddr(s.bars.p_ready);
-  const uint32_t b_turn = saddr(s.bars.turn);
+  const uint32_t b_pv = saddr(s.bars.pv_done);
   const uint32_t b_ofull = saddr(s.bars.o_full), b_ofree = saddr(s.bars.o_free);
 
   if (threadIdx.x == 0) {
@@ -698,10 +713,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_qfull + 8 * i, 1);
       mbar_init(b_qempty + 8 * i, 2);
-      mbar_init(b_sfull + 8 * i, 1);
+      mbar_init(b_sfull + 16 * i, 1);
+      mbar_init(b_sfull + 16 * i + 8, 1);
       mbar_init(b_pready + 16 * i, kGroupThreads);
       mbar_init(b_pready + 16 * i + 8, kGroupThreads);
-      mbar_init(b_turn + 8 * i, kGroupThreads / 32);
+      mbar_init(b_pv + 8 * i, 1);
       mbar_init(b_ofull + 8 * i, 1);
       mbar_init(b_ofree + 8 * i, kGroupThreads);
     }
@@ -729,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t ring = 0;                 // tiles loaded so far
   uint32_t q0_uses = 0, q1_uses = 0; // of the query slots
   uint32_t sn = 0, on = 0;           // steps and runs of the warp's stream
-  uint32_t turns = 0;                // steps of the other stream
+  uint32_t passes = 0;               // that had a step of it
   bool ok = true;
   uint32_t tm = 0;
 
@@ -789,7 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         y0 = (id[0] * p.Hkv + head) * kPageTokens;
         y1 = (id[1] * p.Hkv + head) * kPageTokens;
       };
-      auto load_tile = [&](int tile, const void* map) {
+      // A tile that one stream alone uses is released here for the other, so that
+      // an MMA warp need not look at what is not its stream's.
+      auto load_tile = [&](int tile, const void* map, bool both) {
         if (tile >= from + 32) look_up();
         const bool now = tile >= from;
         const int src = now ? tile - from : tile - from + 32;
@@ -799,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ring >= L::kStages) ok = ok && wait(s, b_empty + 8 * st, (ring / L::kStages - 1) & 1, p);
         ok = __all_sync(kFull, ok);
         if (ok && lane == 0) {
+          if (!both) mbar_arrive(b_empty + 8 * st);
           mbar_expect(bar, L::kTileBytes);
           const uint32_t dst = sb + L::kRing + st * L::kTileBytes;
 #pragma unroll
@@ -819,6 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && lane == 0) {
             const bool one = q.nmem == 1;
             const int rows = one ? p.G : p.G * p.MB;
+            if (w.dual || w.total == 1) mbar_arrive(b_qempty + 8 * sl);   // for the stream without it
             mbar_expect(b_qfull + 8 * sl, (uint32_t)rows * HD * 2);
             const uint32_t dst = sb + L::kQ + sl * L::kTileBytes;
 #pragma unroll
@@ -834,106 +854,115 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kt = 0, vt = 0;
       auto do_k = [&]() {
         if (k.first()) load_q(k);
-        if (k.loads()) load_tile(kt++, &kmap);
+        if (k.loads()) load_tile(kt++, &kmap, k.dual);
         k.next();
       };
       for (int i = 0; i < 2 && i < n_steps && ok; ++i) do_k();
       for (int n = 0; n < n_steps && ok; ++n) {
-        if (v.loads()) load_tile(vt++, &vmap);
+        if (v.loads()) load_tile(vt++, &vmap, v.dual);
         v.next();
         if (ok && n + 2 < n_steps) do_k();
       }
     } else if (warp >= kMmaWarp) {
       // --------------------------------------------------------- MMAs -----
-      // Every lane keeps count, one issues.  Both warps pass over all tiles in the
-      // order of the ring; what a warp's stream does not use, it releases.
+      // Every lane keeps count, one issues.  The warp goes through its stream's
+      // steps, K two of them ahead of V: S of a half takes the place of P while
+      // the softmax has the other half.
       const uint32_t fmt = (1u << 4) | (Half<T>::kFormat << 7) | (Half<T>::kFormat << 10) |
                            ((uint32_t)(kRows >> 4) << 24);
-      const uint32_t id_qk = fmt | ((uint32_t)(kTile >> 3) << 17);
+      const uint32_t id_qk = fmt | ((uint32_t)(kTile / 2 >> 3) << 17);
       const uint32_t id_pv = fmt | (1u << 16) | ((uint32_t)(HD >> 3) << 17);
       Walk k(s.items, n_items, first), v(s.items, n_items, first);
       uint32_t k_at = 0, v_at = 0;     // places in the ring
+      const uint32_t bar_s = b_sfull + 16 * st, bar_p = b_pready + 16 * st;
       // a wait whose outcome is the same in every lane
       auto hold = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(kFull, ok && wait(s, bar, parity, p)); };
       auto hold_tile = [&](uint32_t at) { hold(b_full + 8 * (at % L::kStages), (at / L::kStages) & 1); };
-      auto release = [&](uint32_t bar) {
-        if (ok && lane == 0) mbar_arrive(bar);
-        __syncwarp();
+      auto see_k = [&]() {
+        if (k.loads()) k_at = ring + k.k_place();
       };
-      auto do_k = [&](int n) {
-        if (k.loads()) k_at = ring++;
+      auto leave_k = [&]() {           // to the next step, its stream's or the other's
+        if (k.done()) return;
+        if (k.last()) {
+          const int sl = k.q_slot(0);
+          use_q(sl);
+          if (k.dual) use_q(1);
+        }
+        k.next();
+        see_k();
+      };
+      auto qk = [&](int half) {
         const uint32_t stage = k_at % L::kStages;
         const int sl = k.q_slot(st);
-        if ((n & 1) == st) {
+        if (half == 0) {
           hold_tile(k_at);
           if (k.first_of_stream()) hold(b_qfull + 8 * sl, q_uses(sl) & 1);
           if (!ok) return;
-          tc_after();
-          const uint32_t qa = sb + L::kQ + sl * L::kTileBytes;
-          const uint32_t ka = sb + L::kRing + stage * L::kTileBytes;
+        }
+        tc_after();
+        const uint32_t qa = sb + L::kQ + sl * L::kTileBytes;
+        const uint32_t ka = sb + L::kRing + stage * L::kTileBytes + half * (kTile / 2) * 128;
 #pragma unroll
-          for (int c = 0; c < L::kChunks; ++c)
-            mma_ss4(tm_s, desc_of(qa + c * kRows * 128, 16), desc_of(ka + c * kTile * 128, 16), id_qk, c > 0);
-          tc_commit(b_sfull + 8 * st);
+        for (int c = 0; c < L::kChunks; ++c)
+          mma_ss4(tm_s + half * (kTile / 2), desc_of(qa + c * kRows * 128, 16), desc_of(ka + c * kTile * 128, 16),
+                  id_qk, c > 0);
+        tc_commit(bar_s + 8 * half);
+        if (half == 1) {
           tc_commit(b_empty + 8 * stage);
           if (k.last_of_stream()) tc_commit(b_qempty + 8 * sl);   // the run's last use of a slot
-        } else if (!k.dual) {
-          hold_tile(k_at);
-          release(b_empty + 8 * stage);
         }
-        if (k.last()) {
-          // slots of the run that the stream has not used
-          if (k.dual || (k.total == 1 && (n & 1) != st)) {
-            const int other = k.dual ? st ^ 1 : sl;
-            hold(b_qfull + 8 * other, q_uses(other) & 1);
-            release(b_qempty + 8 * other);
-          }
-          if (k.dual) {
-            use_q(0);
-            use_q(1);
-          } else {
-            use_q(sl);
-          }
-        }
-        k.next();
       };
-      for (int i = 0; i < 2 && i < n_steps && ok; ++i) do_k(i);
-      for (int n = 0; n < n_steps && ok; ++n) {
-        if (v.loads()) v_at = ring++;
-        const uint32_t stage = v_at % L::kStages;
-        if ((n & 1) == st) {
-          hold_tile(v_at);
-          if (v.first_of_stream() && on > 0) hold(b_ofree + 8 * st, (on - 1) & 1);
-          const uint32_t va = sb + L::kRing + stage * L::kTileBytes;
-          for (int half = 0; half < 2; ++half) {
-            hold(b_pready + 16 * st + 8 * half, sn & 1);
-            if (!ok) break;
-            tc_after();
-            mma_ts4(tm_o, tm_s + half * (kTile / 4),
-                    desc_of(va + half * (kTile / 2) * 128, kTile * 128), id_pv,
-                    !(v.first_of_stream() && half == 0));
-          }
-          if (!ok) break;
-          sn += 1;
-          tc_commit(b_empty + 8 * stage);
-          if (v.last_of_stream()) {
-            tc_commit(b_ofull + 8 * st);
-            on += 1;
-          }
-        } else if (!v.dual) {
-          hold_tile(v_at);
-          release(b_empty + 8 * stage);
-        }
+      see_k();
+      if (st == 1 && n_steps > 1) {
+        leave_k();
         v.next();
-        if (ok && n + 2 < n_steps) do_k(n + 2);
       }
+      if (st < n_steps) {
+        qk(0);
+        if (ok) qk(1);
+        leave_k();
+        leave_k();
+      }
+      for (int n = st; n < n_steps && ok; n += 2) {
+        if (v.loads()) v_at = ring + v.v_place(n + 1 < n_steps);
+        else v_at = ring + v.v_place(false);           // of the step before, which shares it
+        const bool more = n + 2 < n_steps;
+        const uint32_t stage = v_at % L::kStages;
+        const uint32_t va = sb + L::kRing + stage * L::kTileBytes;
+        hold_tile(v_at);
+        if (v.first_of_stream() && on > 0) hold(b_ofree + 8 * st, (on - 1) & 1);
+        hold(bar_p, sn & 1);
+        if (!ok) break;
+        tc_after();
+        mma_ts4(tm_o, tm_s, desc_of(va, kTile * 128), id_pv, !v.first_of_stream());
+        if (more) qk(0);
+        else tc_commit(b_pv + 8 * st);
+        hold(bar_p + 8, sn & 1);
+        if (!ok) break;
+        tc_after();
+        mma_ts4(tm_o, tm_s + kTile / 2, desc_of(va + (kTile / 2) * 128, kTile * 128), id_pv, 1);
+        tc_commit(b_empty + 8 * stage);
+        if (v.last_of_stream()) {
+          tc_commit(b_ofull + 8 * st);
+          on += 1;
+        }
+        sn += 1;
+        if (more) {
+          qk(1);
+          leave_k();
+          leave_k();
+          v.next();
+          v.next();
+        }
+      }
+      while (!k.done()) leave_k();
+      ring += 2 * k.tile;
     } else {
       // ------------------------------------------------------ softmax -----
       // A wait that runs out ends no loop here: once one has, all return at once.
       const int r = threadIdx.x & (kGroupThreads - 1); // row
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 lanes
       const uint32_t ts = tm_s + lanes;
-      const uint32_t bar_s = b_sfull + 8 * st, bar_p = b_pready + 16 * st;
       const int j = r / p.G;                           // entry among the rows, less b0
       float m = -INFINITY, l = 0.0f;
       int slot = -2;                                   // the row's partial result; -2: none
@@ -965,47 +994,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int all_see = __reduce_min_sync(kFull, lim);
         for (int u = (st ^ n0) & 1; u < steps; u += 2) {
           const int tile = dual ? u >> 1 : u;
-          const int a = a0 + tile * kTile;             // the tile's first token
-          const bool masked = a < lo || a + kTile > all_see;
-          wait(s, bar_s, sn & 1, p);
-          sn += 1;
+          for (int half = 0; half < 2; ++half) {
+          const uint32_t th = ts + half * (kTile / 2);
+          const int a = a0 + tile * kTile + half * 64;   // the half's first token
+          const bool masked = a < lo || a + 64 > all_see;
+          wait(s, b_sfull + 16 * st + 8 * half, sn & 1, p);
           __syncwarp();
-          // the row's scores, 32 at a time and the next 32 on their way: read twice,
-          // since registers for all of them would leave too few for the rest (what
-          // spills goes to L2: 500 queries on 12845 tokens took 107 us, not 92)
-          uint32_t x[32], y[32];
-          auto mask = [&](uint32_t* v, int c) {        // tokens that are not the row's
-            if (!masked) return;
-            auto bits = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
-            const uint32_t keep = bits(lim - a - c) & ~bits(lo - a - c);
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!((keep >> k) & 1u)) v[k] = 0xff800000u;
-          };
+          uint32_t x[64];                              // the row's scores
           float ref = 0.0f;
           if (busy) {
             tc_after();
-            float t0 = -INFINITY, t1 = -INFINITY;
-            auto largest = [&](const uint32_t* v) {
+            tmem_ld32(th, x);
+            tmem_ld32(th + 32, x + 32);
+            tmem_wait_ld64(x);
+            if (masked) {                              // tokens that are not the row's
+              auto bits = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
 #pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                t0 = max3(t0, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                t1 = max3(t1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+              for (int c = 0; c < 64; c += 32) {
+                const uint32_t keep = bits(lim - a - c) & ~bits(lo - a - c);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!((keep >> k) & 1u)) x[c + k] = 0xff800000u;
               }
-            };
-            tmem_ld32(ts, x);
-            tmem_wait_ld32(x);
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 64) {
-              tmem_ld32(ts + c + 32, y);
-              mask(x, c);
-              largest(x);
-              tmem_wait_ld32(y);
-              tmem_ld32(ts + ((c + 64) & (kTile - 1)), x);   // at the end: the first columns again
-              mask(y, c + 32);
-              largest(y);
-              tmem_wait_ld32(x);
             }
+            float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
+#pragma unroll
+            for (int k = 2; k < 62; k += 4) {
+              t0 = max3(t0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+              t1 = max3(t1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+            }
+            t0 = max3(t0, __uint_as_float(x[62]), __uint_as_float(x[63]));
             const float top = max3(t0, t1, t1) * p.c;
             // a score that is no number, or +infinity, makes the sum NaN
             if (top != -INFINITY) l += top - top;
@@ -1019,21 +1037,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // O of a row without a score so far is 0 already
             if (__any_sync(kFull, some)) {
-              // S of this step was committed after P V of the stream's last
-              // one, so O is at rest
+              // O is at rest behind P V of the stream's half before this one, which
+              // the S that took that half's place was committed after; behind the
+              // last step's first half P V has its own commit
+              if (half == 0) wait(s, b_sfull + 16 * st + 8, sn & 1, p);
+              else if (n0 + u + 2 < n_steps) wait(s, b_sfull + 16 * st, (sn + 1) & 1, p);
+              else wait(s, b_pv + 8 * st, passes & 1, p);
+              __syncwarp();
+              tc_after();
 #pragma unroll 1
               for (int c = 0; c < HD; c += 32) {
-                tmem_ld32(tm_o + lanes + c, y);
-                tmem_wait_ld32(y);
+                uint32_t o[32];
+                tmem_ld32(tm_o + lanes + c, o);
+                tmem_wait_ld32(o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f_old);
-                tmem_st32(tm_o + lanes + c, y);
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f_old);
+                tmem_st32(tm_o + lanes + c, o);
               }
             }
             ref = (m == -INFINITY ? 0.0f : m) - Half<T>::kShift;
           }
-          if (a < lo || (a + kTile > hi && hi % kPageTokens)) {
-            // Clear V's rows of tokens inside the loaded pages that are not the
+          const int before = lo - a, behind = hi - a;
+          if (before > 0 || (behind > 0 && behind < 64)) {
+            // Clear V's rows of tokens inside the half's page that are not the
             // unit's: what lies there is not the sequence's, and 0 x infinity would
             // spoil the row.  The tile's place in the ring is behind the V tiles
             // before and the K tiles of the steps up to the one after that which
@@ -1041,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t at = ring + 2 * (tiles + tile) + 1 + (!dual && n0 + u + 1 < n_steps ? 1 : 0);
             const uint32_t vs = at % L::kStages;
             if (wait(s, b_full + 8 * vs, (at / L::kStages) & 1, p)) {
-              const uint32_t va = sb + L::kRing + vs * L::kTileBytes;
+              const uint32_t va = sb + L::kRing + vs * L::kTileBytes + half * 64 * 128;
               auto clear = [&](int tok0, int tok1) {
                 for (int k = tok0 * 8 + r; k < tok1 * 8; k += kGroupThreads)
 #pragma unroll
@@ -1051,59 +1077,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  "r"(0)
                                  : "memory");
               };
-              if (a < lo) clear(0, min(lo - a, kTile));
-              if (a + kTile > hi)
-                clear(max(hi - a, 0), min(kTile, (max(hi - a, 0) + kPageTokens - 1) / kPageTokens * kPageTokens));
+              clear(0, min(max(before, 0), 64));
+              clear(behind > 0 ? min(behind, 64) : 64, 64);
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             __syncwarp();
           }
-          // The streams take their exponentials in turn: in phase, both would
-          // wait for the special-function units first and for the MMAs then.
-          // Only the pace depends on it.
-          auto my_turn = [&]() {
-            const uint32_t before = turns + (uint32_t)(n0 + u + st) / 2;   // steps of the other stream so far
-            if (before > 0) wait(s, b_turn + 8 * st, (before - 1) & 1, p);
-            __syncwarp();
-          };
-          auto pass_turn = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_turn + 8 * (st ^ 1));
-          };
           if (busy) {
-            my_turn();
             const uint64_t c2 = pair(p.c, p.c), r2 = pair(-ref, -ref);
             uint64_t sum[2] = {0, 0};
-            auto weigh = [&](const uint32_t* v, int c) {
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
               uint32_t o[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
-                uint64_t w = fma2(pair(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, r2);
+                uint64_t w = fma2(pair(__uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1])), c2, r2);
                 float wa, wb;
                 unpair(w, wa, wb);
                 wa = ex2(wa);
                 wb = ex2(wb);
-                w = pair(wa, wb);
-                sum[k & 1] = add2(sum[k & 1], w);
+                sum[k & 1] = add2(sum[k & 1], pair(wa, wb));
                 o[k] = Half<T>::pack(wa, wb);
               }
-              tmem_st16(ts + c / 2, o);        // over columns whose scores have been read
-            };
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 64) {
-              tmem_ld32(ts + c + 32, y);
-              mask(x, c);
-              weigh(x, c);
-              tmem_wait_ld32(y);
-              if (c == 0) tmem_ld32(ts + 64, x);
-              mask(y, c + 32);
-              weigh(y, c + 32);
-              if (c == 0) tmem_wait_ld32(x);
-              else pass_turn();
-              tmem_wait_st();
-              tc_before();
-              mbar_arrive(bar_p + (c ? 8 : 0));
+              tmem_st16(th + c / 2, o);        // over scores that have been read
             }
+            tmem_wait_st();
+            tc_before();
+            mbar_arrive(b_pready + 16 * st + 8 * half);
             float s0, s1, s2, s3;
             unpair(sum[0], s0, s1);
             unpair(sum[1], s2, s3);
@@ -1113,15 +1113,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_after();
 #pragma unroll
               for (int k = 0; k < 32; ++k) x[k] = 0;
-              tmem_st32(ts, x);
-              tmem_st32(ts + 32, x);
+              tmem_st32(th, x);
               tmem_wait_st();
               tc_before();
             }
-            pass_turn();
-            mbar_arrive(bar_p);
-            mbar_arrive(bar_p + 8);
+            mbar_arrive(b_pready + 16 * st + 8 * half);
           }
+          }
+          sn += 1;
         }
         n0 += steps;
         tiles += nt;
@@ -1164,7 +1163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       ring += 2 * tiles;               // the other roles' ring count
-      turns += (uint32_t)(n_steps + st) / 2;
+      passes += n_steps > st;
     }
     __syncthreads();
     ok = ok && *(volatile int*)&s.abort == 0;
