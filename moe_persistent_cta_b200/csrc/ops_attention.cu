@@ -25,12 +25,22 @@
 //
 // One block: a TMA warp streams K and V tiles, two warps issue tcgen05 MMAs,
 // and two groups of four warps hold a softmax row per thread.  S = Q K^T and O
-// live in tensor memory, two of each ("streams"), so that one stream's softmax
-// runs under the other's MMAs.  Each stream has its own MMA warp, since one
-// warp's instructions between two MMAs left the pipe idle.  With more than 128 rows the streams are the
-// two tiles of rows, and each K and V tile serves both; with fewer they are
-// alternate tiles of tokens of the same rows, two partial results.  P goes
-// back to tensor memory over S and is the A operand of P V.
+// live in tensor memory, two of each ("streams"), each with an MMA warp of its
+// own.  A tile's tokens go in two halves: while the softmax has one half of S, the
+// other's P (which goes back to tensor memory over S and is the A operand of P V)
+// is multiplied and replaced by S of the stream's next tile.  With more than 128
+// rows the streams are the two tiles of rows, and each K and V tile serves both;
+// with fewer they are alternate tiles of tokens of the same rows, two partial
+// results.
+//
+// What bounds it: 256 entries on 32768 shared and up to 300 own tokens each (16
+// query heads of 128, 4 KV heads, bf16) take 132 us, 0.52 PFLOP/s, the tensor pipe
+// a third busy.  The MMAs alone, without the softmax, take 119 of them: with 64
+// columns of S each Q K^T reads three times its share from shared memory (Q has no
+// room in tensor memory beside S and O), and with 128 S cannot be replaced by
+// halves (135).  One MMA warp that also passed over the other stream's tiles: 138.
+// Few rows: 8 entries on 8192 tokens 17.7 us, of which 5 find the block's share of
+// the work and 5 add up the partial results.
 //
 // Values that are no numbers.  A masked weight is 0, and 0 x infinity is NaN:
 // V's rows outside a unit's tokens are cleared in shared memory, but a row can
@@ -995,130 +1005,130 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = (st ^ n0) & 1; u < steps; u += 2) {
           const int tile = dual ? u >> 1 : u;
           for (int half = 0; half < 2; ++half) {
-          const uint32_t th = ts + half * (kTile / 2);
-          const int a = a0 + tile * kTile + half * 64;   // the half's first token
-          const bool masked = a < lo || a + 64 > all_see;
-          wait(s, b_sfull + 16 * st + 8 * half, sn & 1, p);
-          __syncwarp();
-          uint32_t x[64];                              // the row's scores
-          float ref = 0.0f;
-          if (busy) {
-            tc_after();
-            tmem_ld32(th, x);
-            tmem_ld32(th + 32, x + 32);
-            tmem_wait_ld64(x);
-            if (masked) {                              // tokens that are not the row's
-              auto bits = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
+            const uint32_t th = ts + half * (kTile / 2);
+            const int a = a0 + tile * kTile + half * 64;   // the half's first token
+            const bool masked = a < lo || a + 64 > all_see;
+            wait(s, b_sfull + 16 * st + 8 * half, sn & 1, p);
+            __syncwarp();
+            uint32_t x[64];                              // the row's scores
+            float ref = 0.0f;
+            if (busy) {
+              tc_after();
+              tmem_ld32(th, x);
+              tmem_ld32(th + 32, x + 32);
+              tmem_wait_ld64(x);
+              if (masked) {                              // tokens that are not the row's
+                auto bits = [](int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; };
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                  const uint32_t keep = bits(lim - a - c) & ~bits(lo - a - c);
+#pragma unroll
+                  for (int k = 0; k < 32; ++k)
+                    if (!((keep >> k) & 1u)) x[c + k] = 0xff800000u;
+                }
+              }
+              float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
+#pragma unroll
+              for (int k = 2; k < 62; k += 4) {
+                t0 = max3(t0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                t1 = max3(t1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+              }
+              t0 = max3(t0, __uint_as_float(x[62]), __uint_as_float(x[63]));
+              const float top = max3(t0, t1, t1) * p.c;
+              // a score that is no number, or +infinity, makes the sum NaN
+              if (top != -INFINITY) l += top - top;
+              const bool grow = top > m + kRescale;      // also the first score of a row
+              const bool some = grow && m != -INFINITY;
+              float f_old = 1.0f;
+              if (grow) {
+                f_old = ex2(m - top);                    // 0 for the first
+                l *= f_old;
+                m = top;
+              }
+              // O of a row without a score so far is 0 already
+              if (__any_sync(kFull, some)) {
+                // O is at rest behind P V of the stream's half before this one, which
+                // the S that took that half's place was committed after; behind the
+                // last step's first half P V has its own commit
+                if (half == 0) wait(s, b_sfull + 16 * st + 8, sn & 1, p);
+                else if (n0 + u + 2 < n_steps) wait(s, b_sfull + 16 * st, (sn + 1) & 1, p);
+                else wait(s, b_pv + 8 * st, passes & 1, p);
+                __syncwarp();
+                tc_after();
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(tm_o + lanes + c, o);
+                  tmem_wait_ld32(o);
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f_old);
+                  tmem_st32(tm_o + lanes + c, o);
+                }
+              }
+              ref = (m == -INFINITY ? 0.0f : m) - Half<T>::kShift;
+            }
+            const int before = lo - a, behind = hi - a;
+            if (before > 0 || (behind > 0 && behind < 64)) {
+              // Clear V's rows of tokens inside the half's page that are not the
+              // unit's: what lies there is not the sequence's, and 0 x infinity would
+              // spoil the row.  The tile's place in the ring is behind the V tiles
+              // before and the K tiles of the steps up to the one after that which
+              // loaded it.
+              const uint32_t at = ring + 2 * (tiles + tile) + 1 + (!dual && n0 + u + 1 < n_steps ? 1 : 0);
+              const uint32_t vs = at % L::kStages;
+              if (wait(s, b_full + 8 * vs, (at / L::kStages) & 1, p)) {
+                const uint32_t va = sb + L::kRing + vs * L::kTileBytes + half * 64 * 128;
+                auto clear = [&](int tok0, int tok1) {
+                  for (int k = tok0 * 8 + r; k < tok1 * 8; k += kGroupThreads)
+#pragma unroll
+                    for (int c = 0; c < L::kChunks; ++c)
+                      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                       va + c * kTile * 128 + k * 16),
+                                   "r"(0)
+                                   : "memory");
+                };
+                clear(0, min(max(before, 0), 64));
+                clear(behind > 0 ? min(behind, 64) : 64, 64);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              }
+              __syncwarp();
+            }
+            if (busy) {
+              const uint64_t c2 = pair(p.c, p.c), r2 = pair(-ref, -ref);
+              uint64_t sum[2] = {0, 0};
 #pragma unroll
               for (int c = 0; c < 64; c += 32) {
-                const uint32_t keep = bits(lim - a - c) & ~bits(lo - a - c);
+                uint32_t o[16];
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (!((keep >> k) & 1u)) x[c + k] = 0xff800000u;
+                for (int k = 0; k < 16; ++k) {
+                  uint64_t w = fma2(pair(__uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1])), c2, r2);
+                  float wa, wb;
+                  unpair(w, wa, wb);
+                  wa = ex2(wa);
+                  wb = ex2(wb);
+                  sum[k & 1] = add2(sum[k & 1], pair(wa, wb));
+                  o[k] = Half<T>::pack(wa, wb);
+                }
+                tmem_st16(th + c / 2, o);        // over scores that have been read
               }
-            }
-            float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
-#pragma unroll
-            for (int k = 2; k < 62; k += 4) {
-              t0 = max3(t0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-              t1 = max3(t1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
-            }
-            t0 = max3(t0, __uint_as_float(x[62]), __uint_as_float(x[63]));
-            const float top = max3(t0, t1, t1) * p.c;
-            // a score that is no number, or +infinity, makes the sum NaN
-            if (top != -INFINITY) l += top - top;
-            const bool grow = top > m + kRescale;      // also the first score of a row
-            const bool some = grow && m != -INFINITY;
-            float f_old = 1.0f;
-            if (grow) {
-              f_old = ex2(m - top);                    // 0 for the first
-              l *= f_old;
-              m = top;
-            }
-            // O of a row without a score so far is 0 already
-            if (__any_sync(kFull, some)) {
-              // O is at rest behind P V of the stream's half before this one, which
-              // the S that took that half's place was committed after; behind the
-              // last step's first half P V has its own commit
-              if (half == 0) wait(s, b_sfull + 16 * st + 8, sn & 1, p);
-              else if (n0 + u + 2 < n_steps) wait(s, b_sfull + 16 * st, (sn + 1) & 1, p);
-              else wait(s, b_pv + 8 * st, passes & 1, p);
-              __syncwarp();
-              tc_after();
-#pragma unroll 1
-              for (int c = 0; c < HD; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(tm_o + lanes + c, o);
-                tmem_wait_ld32(o);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f_old);
-                tmem_st32(tm_o + lanes + c, o);
-              }
-            }
-            ref = (m == -INFINITY ? 0.0f : m) - Half<T>::kShift;
-          }
-          const int before = lo - a, behind = hi - a;
-          if (before > 0 || (behind > 0 && behind < 64)) {
-            // Clear V's rows of tokens inside the half's page that are not the
-            // unit's: what lies there is not the sequence's, and 0 x infinity would
-            // spoil the row.  The tile's place in the ring is behind the V tiles
-            // before and the K tiles of the steps up to the one after that which
-            // loaded it.
-            const uint32_t at = ring + 2 * (tiles + tile) + 1 + (!dual && n0 + u + 1 < n_steps ? 1 : 0);
-            const uint32_t vs = at % L::kStages;
-            if (wait(s, b_full + 8 * vs, (at / L::kStages) & 1, p)) {
-              const uint32_t va = sb + L::kRing + vs * L::kTileBytes + half * 64 * 128;
-              auto clear = [&](int tok0, int tok1) {
-                for (int k = tok0 * 8 + r; k < tok1 * 8; k += kGroupThreads)
-#pragma unroll
-                  for (int c = 0; c < L::kChunks; ++c)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                     va + c * kTile * 128 + k * 16),
-                                 "r"(0)
-                                 : "memory");
-              };
-              clear(0, min(max(before, 0), 64));
-              clear(behind > 0 ? min(behind, 64) : 64, 64);
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            __syncwarp();
-          }
-          if (busy) {
-            const uint64_t c2 = pair(p.c, p.c), r2 = pair(-ref, -ref);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-              uint32_t o[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                uint64_t w = fma2(pair(__uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1])), c2, r2);
-                float wa, wb;
-                unpair(w, wa, wb);
-                wa = ex2(wa);
-                wb = ex2(wb);
-                sum[k & 1] = add2(sum[k & 1], pair(wa, wb));
-                o[k] = Half<T>::pack(wa, wb);
-              }
-              tmem_st16(th + c / 2, o);        // over scores that have been read
-            }
-            tmem_wait_st();
-            tc_before();
-            mbar_arrive(b_pready + 16 * st + 8 * half);
-            float s0, s1, s2, s3;
-            unpair(sum[0], s0, s1);
-            unpair(sum[1], s2, s3);
-            l += (s0 + s1) + (s2 + s3);
-          } else {
-            if (own) {                 // other entries' tokens: no weight
-              tc_after();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = 0;
-              tmem_st32(th, x);
               tmem_wait_st();
               tc_before();
+              mbar_arrive(b_pready + 16 * st + 8 * half);
+              float s0, s1, s2, s3;
+              unpair(sum[0], s0, s1);
+              unpair(sum[1], s2, s3);
+              l += (s0 + s1) + (s2 + s3);
+            } else {
+              if (own) {                 // other entries' tokens: no weight
+                tc_after();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = 0;
+                tmem_st32(th, x);
+                tmem_wait_st();
+                tc_before();
+              }
+              mbar_arrive(b_pready + 16 * st + 8 * half);
             }
-            mbar_arrive(b_pready + 16 * st + 8 * half);
-          }
           }
           sn += 1;
         }

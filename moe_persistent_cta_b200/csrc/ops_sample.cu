@@ -26,7 +26,12 @@
 //    split in four, again and again, by exact sums.
 // Few tokens are ordered by counting, for each, the larger ones: all threads read
 // the same word at a time, and there is no chain of barriers (1024 tokens: 7.9 us
-// by a bitonic sort).
+// by a bitonic sort, 1.6 by counting).
+//
+// What bounds it: the passes over shared memory, about 2 us each for 151552 tokens
+// over 8 blocks, and for the passes that weigh every token 14 64-bit operations a
+// token (5 us).  256 rows of 151552 with mixed rules take 215 us (0.72 TB/s of
+// logits), one row of 1024 7.6 us.
 #include <cooperative_groups.h>
 
 #include <mutex>
