@@ -1257,8 +1257,11 @@ template <int W>
 constexpr int kJoinWarps = W > 4 ? W : 4;   // of a block
 
 template <typename T, int HD, int W>
-__global__ void __launch_bounds__(32 * kJoinWarps<W>) join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps<W>, W > 1 ? 1 : 8) join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int C = HD / 32;
+  // Many rows: few shares each, and room for more warps matters more (8000 rows:
+  // 2 us less than with 8).
+  constexpr int kAhead = W > 1 ? 8 : 4;
   __shared__ float s_acc[W > 1 ? W : 1][HD];
   __shared__ float2 s_ml[W > 1 ? W : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % W;
@@ -1314,11 +1317,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>) join_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < C; ++i) acc[i] *= fo;
       const int shares = min(32, (n - i0 + W - 1) / W);
-      // eight shares' rows on their way at once
-      for (int i1 = 0; i1 < shares; i1 += 8) {
-        float fi[8], v[8][C];
+      // kAhead shares' rows on their way at once
+      for (int i1 = 0; i1 < shares; i1 += kAhead) {
+        float fi[kAhead], v[kAhead][C];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
           fi[u] = __shfl_sync(kFull, f, i1 + u);       // 0 behind the last
           const float li = __shfl_sync(kFull, ml.y, i1 + u);
           const float* src = p.part + __shfl_sync(kFull, (unsigned long long)at_row, i1 + u) * HD + lane * C;
@@ -1340,7 +1343,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>) join_kernel(const __grid_c
           }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < kAhead; ++u)
 #pragma unroll
           for (int k = 0; k < C; ++k) acc[k] = fmaf(v[u][k], fi[u], acc[k]);
       }
@@ -1425,8 +1428,10 @@ int sm_count(int device) {
   return count[device];
 }
 
-// Rows up to which eight warps join one: few rows have many shares each.
-constexpr unsigned kWideJoin = 2048;
+// Rows up to which eight warps join one: few rows have many shares each, and as
+// many blocks run at once (128 rows: 17.4 us in all; 976 rows: 41 us, with one
+// warp a row 31).
+constexpr unsigned kWideJoin = 448;
 
 constexpr int kMaxBlocks = 160;      // at least the device's multiprocessors
 
