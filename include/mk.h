@@ -401,7 +401,8 @@ mk_status mk_rope_append(const mk_rope_append_args* args, void* stream);
  * entry then sees nothing) or a page id out of range (its keys and values read
  * as zero) is a device-side fault.  What other entries' tokens hold, infinities
  * and NaN included, does not reach an entry's row.  n_q_heads is a
- * multiple of n_kv_heads, at most 64 times it; batch is at most 4096.       */
+ * multiple of n_kv_heads, at most 64 times it; batch and n_groups are at most
+ * 4096, batch x n_kv_heads x (max_pages + 4) is below 2^31.                 */
 typedef struct mk_prefix_attention_args {
   int32_t device;
   int32_t batch, n_groups, max_pages, n_pages;

@@ -190,3 +190,10 @@ def test_sampling_rules():
     assert r["top_k"].dtype == torch.int32 and set(r) == {"temperature", "top_k"}
     with pytest.raises(ValueError):
         serving.sampling_rules(dict(top_q=0.5), 3, "cpu")
+
+
+def test_attention_line_of_tiles_fits_32_bits():
+    big = dict(batch=4096, n_kv_heads=8, n_q_heads=8, q_token_stride=512, n_pages=8)
+    assert mk.lib.mk_prefix_attention_workspace(byref(attention_args(max_pages=65531, **big))) > 0
+    assert mk.lib.mk_prefix_attention_workspace(byref(attention_args(max_pages=65532, **big))) == 0
+    assert mk.lib.mk_prefix_attention(byref(attention_args(max_pages=65532, **big)), None) == mk.MK_ERR_CAPACITY
