@@ -660,3 +660,26 @@ def test_sample_top_p_where_the_weights_lie_flat():
     for p in (0.05, 0.3, 0.62, 0.9, 0.999):
         sample_case(x, r.random(4), p=[p] * 4)
     sample_case(x.astype(np.float16), r.random(4), p=[0.6] * 4, dt="fp16")
+
+
+@pytest.mark.parametrize("b,v", [(2, 40000), (9, 40000), (3, 5000)])
+def test_sample_over_clusters_captured(b, v):
+    # clusters of 16, 8 and 4 blocks; two graphs alive, replayed with other inputs
+    g = gen(60 + b)
+    graphs = []
+    for _ in range(2):
+        s = dict(x=torch.randn((b, v), generator=g).to(DEV), u=torch.rand(b, generator=g).to(DEV),
+                 p=torch.full((b,), 0.9, device=DEV), k=i32([0, 40, 600] * 3)[:b], t=i32([-9] * b))
+        kw = dict(top_p=s["p"], top_k=s["k"])
+        ops.sample(s["x"], s["u"], **kw)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            ops.sample(s["x"], s["u"], tokens=s["t"], **kw)
+        graphs.append((graph, s, kw))
+    for _ in range(3):
+        for graph, s, kw in graphs:
+            s["x"].copy_(torch.randn((b, v), generator=g))
+            s["u"].copy_(torch.rand(b, generator=g))
+            graph.replay()
+            assert torch.equal(s["t"], ops.sample(s["x"], s["u"], **kw))
