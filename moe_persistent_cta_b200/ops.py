@@ -6,6 +6,8 @@ Each function checks its arguments, hands raw device pointers to ``libmk.so``
 and returns after the launch; all computation happens in the library's
 kernels.  Tensors live on one CUDA device, which need not be the current one;
 ``stream`` is a torch stream of that device (its current stream by default).
+Outputs that a function allocates are made and cleared on that stream; tensors
+that the caller passes have to be ready there, and to live until it has used them.
 A call keeps nothing: it may be captured into a graph, and calls on other
 streams may overlap it as long as they write other tensors.
 """
@@ -90,6 +92,18 @@ def _stream(stream, dev: int) -> int:
     return stream.cuda_stream
 
 
+def _output(make, shape, dtype, device, stream) -> torch.Tensor:
+    """An output of the caller's, made (and filled) on the call's stream: its
+    memory is that stream's, and so is the order of filling and kernel.  The
+    caller's current stream is noted, which may use it when the call's is past it."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _status(status: Optional[Status], dev: int) -> int:
     if status is None:
         return 0
@@ -167,6 +181,7 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     ``rope_frequencies``.  Returns q_out ([tokens][query heads][hd] of the
     pools' type; allocated if None, may be q itself), None without queries."""
     dev = _cuda(k, "k")
+    handle = _stream(stream, dev)
     pool, n_pages, hkv, hd = _pools(k_pool, v_pool, dev)
     dtype, shape = k.dtype, k.shape
     t = shape[0]
@@ -189,7 +204,7 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
         if t and qs[2] != 1:
             raise ValueError("the columns of q must be adjacent")
         if q_out is None:
-            q_out = torch.empty((t, hq, hd), dtype=pool, device=q.device)
+            q_out = _output(torch.empty, (t, hq, hd), pool, q.device, stream)
         elif (q_out.shape != shape or not q_out.is_contiguous() or q_out.dtype is not pool
               or q_out.get_device() != dev):
             raise ValueError("q_out must be contiguous, shaped like q and of the pools' type and device")
@@ -212,7 +227,6 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
         out_at, k_pool.data_ptr(), v_pool.data_ptr(), inv_freq.data_ptr(),
         _array(positions, _I32, "positions", dev, (t,)), 0 if seq is None else _array(seq, _I32, "seq", dev, (t,)),
         _array(page_table, _I32, "page_table", dev, table), _status(status, dev))
-    handle = _stream(stream, dev)
     if t:
         rc = mk.lib.mk_rope_append(a, handle)
         if rc:
@@ -240,6 +254,7 @@ def prefix_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
     are then zero); lse, if given, float32[batch][query heads], receives the log
     of each row's sum of exponentials."""
     dev = _cuda(q, "q")
+    handle = _stream(stream, dev)
     dtype, n_pages, hkv, hd = _pools(k_pool, v_pool, dev)
     shape = q.shape
     if len(shape) != 3 or shape[2] != hd:
@@ -256,11 +271,10 @@ def prefix_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
         raise ValueError("page_table must be [batch][pages per row], group_start and prefix_lens flat")
     n, pages = prefix_lens.shape[0], page_table.shape[1]
     if out is None:
-        out = torch.zeros(shape, dtype=dtype, device=q.device)
+        out = _output(torch.zeros, shape, dtype, q.device, stream)
     elif (out.shape != shape or not out.is_contiguous() or out.dtype is not dtype
           or out.get_device() != dev):
         raise ValueError("out must be contiguous with q's shape, type and device")
-    handle = _stream(stream, dev)
     if b == 0 or n == 0:
         return out
     # the workspace is this call's own; torch hands its memory on in stream order
@@ -303,6 +317,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch
     logprobs, if given, float32[batch], receives each drawn token's log-probability
     among the kept ones."""
     dev = _cuda(logits, "logits")
+    handle = _stream(stream, dev)
     kind = _TYPE.get(logits.dtype)
     if kind is None:
         raise TypeError("logits must be float32, bfloat16 or float16")
@@ -315,7 +330,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch
         raise ValueError("the columns of logits must be adjacent")
     rows = (b,)
     if tokens is None:
-        tokens = torch.empty(b, dtype=_I32, device=logits.device)
+        tokens = _output(torch.empty, rows, _I32, logits.device, stream)
     a = _PACK_SAMPLE(
         dev, b, v, kind, logits.data_ptr(), ls[0], _array(u, _F32, "u", dev, rows),
         0 if temperature is None else _array(temperature, _F32, "temperature", dev, rows),
@@ -324,7 +339,6 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch
         0 if min_p is None else _array(min_p, _F32, "min_p", dev, rows),
         _array(tokens, _I32, "tokens", dev, rows),
         0 if logprobs is None else _array(logprobs, _F32, "logprobs", dev, rows), _status(status, dev))
-    handle = _stream(stream, dev)
     if b:
         rc = mk.lib.mk_sample(a, handle)
         if rc:

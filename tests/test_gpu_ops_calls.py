@@ -1,0 +1,108 @@
+"""How the serving operators' Python functions are called on the GPU: other
+streams than the current one, outputs that the functions allocate, status words,
+workspaces and waits that run out."""
+
+import math
+
+import pytest
+import torch
+
+from moe_persistent_cta_b200 import mk, ops
+from tests import ops_oracle
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BUSY = 200_000_000          # cycles: about a tenth of a second
+
+
+def i32(x):
+    return torch.as_tensor(x, dtype=torch.int32).to(DEV)
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def attention_case(seed=1, lens=(90, 200, 131), hq=4, hkv=2, hd=64, dtype=torch.bfloat16, prefix=64):
+    """Entries of one group, `prefix` tokens shared; the arguments and the 64-bit result."""
+    g = gen(seed)
+    b, width = len(lens), max(lens) // 64 + 1
+    kp, vp = (torch.randn((b * width, hkv, 64, hd), generator=g).to(dtype) for _ in range(2))
+    q = torch.randn((b, hq, hd), generator=g).to(dtype)
+    table = torch.randperm(b * width, generator=g).view(b, width).to(torch.int32)
+    pos = [n - 1 for n in lens]
+    want = ops_oracle.attention(q, kp, vp, table, pos, [0, b], [prefix], 1 / math.sqrt(hd))
+    args = [x.to(DEV) for x in (q, kp, vp, table)] + [i32(pos), i32([0, b]), i32([prefix])]
+    return args, want
+
+
+def check_attention(out, want, dtype=torch.bfloat16):
+    # P's rounding moves a row by half a step of the weighted |v|, the output's by half a
+    # step of itself; 32-bit scores and sums by 2e-5 (1 + the largest score)
+    exact, _, mass, high = want
+    h = torch.finfo(dtype).eps / 2
+    bound = h * mass + h * exact.abs() + 2e-5 * (1 + high[..., None]) * mass + 1e-30
+    assert ((out.cpu().double() - exact).abs() <= bound).all()
+
+
+def check_tokens(tokens, logits, u):
+    x, u = logits.cpu().numpy(), u.cpu().numpy()
+    assert tokens.cpu().tolist() == [ops_oracle.sample(x[b], float(u[b]))[0] for b in range(len(u))]
+
+
+# ---------------------------------------------------------------- streams --
+
+def test_outputs_of_a_call_on_another_stream_than_the_current_one():
+    """The functions' own outputs, with the current stream behind its work: what
+    that stream does later reaches neither their values nor their memory."""
+    args, want = attention_case()
+    logits = torch.randn((5, 700), generator=gen(2)).to(DEV)
+    u = torch.rand(5, generator=gen(3)).to(DEV)
+    x = torch.randn((6, 4, 64), generator=gen(4)).to(torch.bfloat16).to(DEV)
+    pool = torch.zeros((2, 1, 64, 64), dtype=torch.bfloat16, device=DEV)
+    rope = (x[:, :2], x[:, 2:3], x[:, 3:], i32(range(6)), i32([[0, 1]]), pool, pool.clone(),
+            ops.rope_frequencies(64, device=DEV)[0])
+    kw = dict(seq=i32([0] * 6))
+    side = torch.cuda.Stream()
+    plain_q = ops.rope_append(*rope, **kw)
+    ops.prefix_attention(*args, stream=side)             # loads the modules and fills the allocator's pools
+    ops.sample(logits, u, stream=side)
+    ops.rope_append(*rope, stream=side, **kw)
+    torch.cuda.synchronize()
+    # blocks that go back to the current stream's pool with a write of that stream still to come
+    late = [torch.empty_like(plain_q), torch.empty(5, dtype=torch.int32, device=DEV), torch.empty_like(args[0])]
+    for t in late:
+        t.fill_(7)                                       # loads the kernel, which may wait for the device
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    for t in late:
+        t.fill_(77)
+    del late, t
+    out = ops.prefix_attention(*args, stream=side)
+    tokens = ops.sample(logits, u, stream=side)
+    q_out = ops.rope_append(*rope, stream=side, **kw)
+    torch.cuda.synchronize()
+    check_attention(out, want)
+    check_tokens(tokens, logits, u)
+    assert torch.equal(q_out, plain_q)
+
+
+def test_outputs_of_another_stream_outlive_their_release():
+    """An output released while the current stream still reads it is not handed
+    out again on the call's stream before that read."""
+    logits = torch.randn((64, 300), generator=gen(5)).to(DEV)
+    u = torch.rand(64, generator=gen(6)).to(DEV)
+    other = torch.rand(64, generator=gen(7)).to(DEV)
+    side = torch.cuda.Stream()
+    ops.sample(logits, u, stream=side)
+    torch.cuda.synchronize()
+    tokens = ops.sample(logits, u, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(BUSY)
+    kept = torch.empty_like(tokens).copy_(tokens)
+    del tokens
+    again = ops.sample(logits, other, stream=side)
+    torch.cuda.synchronize()
+    check_tokens(kept, logits, u)
+    check_tokens(again, logits, other)
