@@ -34,20 +34,29 @@ _OPS = {mk.MK_OP_ROPE_APPEND: "rope_append", mk.MK_OP_PREFIX_ATTENTION: "prefix_
 
 class Status:
     """Device word that latches the first device-side fault of the calls that
-    name it (``status=``): a page id, position or parameter out of range."""
+    name it (``status=``): a page id, position or parameter out of range.  Calls
+    on any stream may name it, captured ones too; it is made outside a capture."""
 
     def __init__(self, device):
         self.word = torch.zeros(8, dtype=_I32, device=device)
+        # cleared before any stream's call can name it
+        torch.cuda.current_stream(self.word.device).synchronize()
 
-    def check(self):
-        """Synchronize, read and clear: (status, [operator, entry, value, limit])."""
-        w = self.word.tolist()
-        if w[0] != mk.MK_OK:
-            self.word.zero_()
+    def check(self, stream=None):
+        """Wait for the device's work (with ``stream``: for that stream's alone),
+        read and clear: (status, [operator, entry, value, limit])."""
+        if stream is None:
+            torch.cuda.synchronize(self.word.device)
+            stream = torch.cuda.current_stream(self.word.device)
+        with torch.cuda.stream(stream):
+            w = self.word.tolist()
+            if w[0] != mk.MK_OK:
+                self.word.zero_()
+                stream.synchronize()
         return w[0], w[1:5]
 
-    def check_ok(self) -> None:
-        rc, detail = self.check()
+    def check_ok(self, stream=None) -> None:
+        rc, detail = self.check(stream)
         if rc != mk.MK_OK:
             raise mk.MKError(rc, _OPS.get(detail[0], "device status"), detail)
 

@@ -106,3 +106,57 @@ def test_outputs_of_another_stream_outlive_their_release():
     torch.cuda.synchronize()
     check_tokens(kept, logits, u)
     check_tokens(again, logits, other)
+
+
+# ----------------------------------------------------------------- status --
+
+def test_status_waits_for_calls_on_other_streams():
+    logits = torch.randn((3, 50), generator=gen(8)).to(DEV)
+    bad = torch.tensor([0.5, 1.5, 0.5], device=DEV)      # a number outside [0, 1)
+    side = torch.cuda.Stream()
+    status = ops.Status(DEV)
+    ops.sample(logits, bad, stream=side, status=status)  # loads the module
+    assert status.check()[0] == mk.MK_ERR_DEVICE
+    for wait_for in (None, side):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(BUSY)
+        ops.sample(logits, bad, stream=side, status=status)
+        rc, detail = status.check() if wait_for is None else status.check(wait_for)
+        assert rc == mk.MK_ERR_DEVICE and detail[:2] == [mk.MK_OP_SAMPLE, 1]
+        status.check_ok(wait_for)                        # cleared
+    # the clearing is past before a call on another stream can latch the next one
+    ops.sample(logits, bad, stream=side, status=status)
+    assert status.check()[0] == mk.MK_ERR_DEVICE
+
+
+def test_status_word_is_clear_before_its_first_use():
+    logits = torch.randn((1, 50), generator=gen(8)).to(DEV)
+    bad = torch.tensor([-1.0], device=DEV)
+    side = torch.cuda.Stream()
+    ops.sample(logits, bad, stream=side)
+    torch.zeros(8, dtype=torch.int32, device=DEV)        # loads the kernels
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    status = ops.Status(DEV)
+    ops.sample(logits, bad, stream=side, status=status)
+    side.synchronize()
+    assert status.check()[0] == mk.MK_ERR_DEVICE
+
+
+def test_status_of_a_captured_call():
+    logits = torch.randn((2, 50), generator=gen(9)).to(DEV)
+    u = torch.tensor([0.5, 0.25], device=DEV)
+    status, tokens = ops.Status(DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    ops.sample(logits, u, tokens=tokens, status=status)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.sample(logits, u, tokens=tokens, status=status)
+    side = torch.cuda.Stream()
+    for good in (True, False, True):
+        u.copy_(torch.tensor([0.5, 0.25 if good else math.nan]))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(BUSY // 10)
+            graph.replay()
+        rc, detail = status.check()
+        assert (rc == mk.MK_OK) if good else (rc == mk.MK_ERR_DEVICE and detail[1] == 1)
