@@ -474,7 +474,11 @@ mk_status mk_sample(const mk_sample_args* args, void* stream);
  * fused step's counters on short ones.  plan_len of the schedule does not limit
  * the lengths, the page table does.  A fault of the two operators is reported by
  * mk_check as {code, operator, entry, value, limit}.  The first call after
- * mk_build_schedule allocates, so it cannot be captured into a graph.        */
+ * mk_build_schedule allocates.
+ * A context's steps count on in its device memory from call to call, and the
+ * host knows how far: none of them (fused, shared or sampled) may be captured
+ * into a graph and replayed.  This call and mk_decode_sample return
+ * MK_ERR_STATE on a stream that is being captured.                          */
 mk_status mk_decode_step_shared(mk_ctx* ctx, const int32_t* tokens, const int32_t* positions,
                                 const int32_t* page_table, const int32_t* seq_lens,
                                 int32_t n_groups, const int32_t* group_start,

@@ -594,6 +594,14 @@ mk_status mk_decode_greedy(mk_ctx* c, int32_t n_steps, int32_t* tokens, int32_t*
   return MK_OK;
 }
 
+// A step's epoch is an argument of its launches: replayed from a graph, the
+// step would wait for counts that are long passed.  MK_ERR_STATE in a capture.
+static mk_status refuse_capture(cudaStream_t st) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  MK_CUDA(cudaStreamIsCapturing(st, &capture));
+  return capture == cudaStreamCaptureStatusNone ? MK_OK : MK_ERR_STATE;
+}
+
 // The fused list cut at its attention tasks, which are contiguous per layer:
 // what lies between them runs as one launch each.  Those tasks' counter
 // arrivals are added by one kernel ahead of the step.
@@ -653,6 +661,7 @@ static mk_status launch_shared(mk_ctx* c, const int32_t* tokens, const int32_t* 
   if (n_groups < 1 || n_groups > c->B || !group_start || !prefix_lens) return MK_ERR_INVALID;
   MK_CUDA(cudaSetDevice(c->device));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MK_TRY(refuse_capture(st));
   MK_TRY(prepare_shared(c));
   const Shape& s = c->shape;
   mk_prefix_attention_args at{};
@@ -767,6 +776,10 @@ mk_status mk_decode_sample(mk_ctx* c, int32_t n_steps, int32_t* tokens, int32_t*
   a.min_p = how->min_p;
   a.status = c->d_status;
   if (a.vocab > MK_SAMPLE_MAX_VOCAB) return MK_ERR_CAPACITY;
+  if (n_steps > 0) {
+    MK_CUDA(cudaSetDevice(c->device));
+    MK_TRY(refuse_capture(static_cast<cudaStream_t>(stream)));
+  }
   for (int32_t i = 0; i < n_steps; ++i) {
     const size_t at = (size_t)i * c->B;
     if (how->n_groups > 0)

@@ -1,0 +1,34 @@
+"""How the decode loop's shared and sampled steps are called on the GPU: captures,
+arguments that do not fit the schedule, faults outside a step, other streams."""
+
+import numpy as np
+import pytest
+import torch
+
+from moe_persistent_cta_b200 import configs, engine, mk, ops, serving, synth
+from tests.gpu_common import MAX_ABS, REL_L2, TinyRig, compare_logits, to_dev
+from tests.test_gpu_shared import DEV, i32, shared_rig, shared_step
+
+pytestmark = pytest.mark.gpu
+
+
+def test_steps_refuse_a_capture():
+    r, start, ends = shared_rig([100, 90], [2], [64])
+    try:
+        ref = r.oracle_step()
+        args = (r.i32(r.tokens), r.i32(r.lens), r.table.to(DEV), r.i32(r.lens))
+        out, u = torch.zeros((1, 2), dtype=torch.int32, device=DEV), torch.rand((1, 2), device=DEV)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for call in (lambda: r.dec.step_shared(*args, start, ends, r.logits),
+                         lambda: r.dec.sample(1, *args, r.logits, out, u),
+                         lambda: r.dec.sample(1, *args, r.logits, out, u, group_start=start, prefix_lens=ends)):
+                with pytest.raises(mk.MKError) as e:
+                    call()
+                assert e.value.status == mk.MK_ERR_STATE
+            out.fill_(5)
+        graph.replay()
+        err, rel = compare_logits(shared_step(r, start, ends), ref)
+        assert err <= MAX_ABS and rel <= REL_L2 and (out == 5).all()
+    finally:
+        r.close()
