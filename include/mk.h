@@ -476,7 +476,10 @@ mk_status mk_sample(const mk_sample_args* args, void* stream);
  * mk_check as {code, operator, entry, value, limit}.  The first call after
  * mk_build_schedule allocates.
  * A context's steps count on in its device memory from call to call, and the
- * host knows how far: none of them (fused, shared or sampled) may be captured
+ * host knows how far.  If a launch of this call fails behind its first, they
+ * stand apart: every step then returns MK_ERR_STATE until mk_check or
+ * mk_build_schedule has cleared the counters.
+ * For the same reason none of the steps (fused, shared or sampled) may be captured
  * into a graph and replayed.  This call and mk_decode_sample return
  * MK_ERR_STATE on a stream that is being captured.                          */
 mk_status mk_decode_step_shared(mk_ctx* ctx, const int32_t* tokens, const int32_t* positions,

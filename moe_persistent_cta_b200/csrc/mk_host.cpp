@@ -78,6 +78,7 @@ struct mk_ctx {
   unsigned long long timeout_ns = 2000ull * 1000ull * 1000ull;
   cudaStream_t last_stream = nullptr;
   bool launched = false;   // a step was launched on last_stream
+  bool cut_short = false;  // a launch of a step failed behind its first: counters are short
   Params base{};
 };
 
@@ -495,6 +496,7 @@ mk_status mk_build_schedule(mk_ctx* c, int batch, const int32_t* seq_lens,
   c->max_chunks = plan.max_chunks;
   c->max_pages = max_pages_per_seq;
   c->epoch = 0;
+  c->cut_short = false;
   c->have_schedule = true;
   MK_CUDA(cudaDeviceSynchronize());
   return MK_OK;
@@ -512,7 +514,7 @@ static mk_status launch_step(mk_ctx* c, const int32_t* tokens, const int32_t* po
                              const int32_t* page_table, const int32_t* seq_lens, float* logits,
                              void* stream, bool unfused, const Greedy* greedy = nullptr) {
   if (!c) return MK_ERR_INVALID;
-  if (!c->have_schedule) return MK_ERR_STATE;
+  if (!c->have_schedule || c->cut_short) return MK_ERR_STATE;
   if (!tokens || !positions || !page_table || !seq_lens || !logits) return MK_ERR_INVALID;
   MK_CUDA(cudaSetDevice(c->device));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -656,7 +658,7 @@ static mk_status launch_shared(mk_ctx* c, const int32_t* tokens, const int32_t* 
                                const int32_t* group_start, const int32_t* prefix_lens, float* logits,
                                void* stream) {
   if (!c) return MK_ERR_INVALID;
-  if (!c->have_schedule) return MK_ERR_STATE;
+  if (!c->have_schedule || c->cut_short) return MK_ERR_STATE;
   if (!tokens || !positions || !page_table || !seq_lens || !logits) return MK_ERR_INVALID;
   if (n_groups < 1 || n_groups > c->B || !group_start || !prefix_lens) return MK_ERR_INVALID;
   MK_CUDA(cudaSetDevice(c->device));
@@ -718,8 +720,9 @@ static mk_status launch_shared(mk_ctx* c, const int32_t* tokens, const int32_t* 
   p.n_ctas = c->plan.n_ctas;
   MK_CUDA(mk::ops::add_to_counters(c->d_counters, static_cast<const int32_t*>(c->shared_counters.ptr),
                                    c->n_shared_counters, st));
-  // from here on a step that stops part-way leaves counters short: mk_check's
+  // from here on a step whose launches stop part-way leaves counters short: mk_check's
   // reset is needed, as after a device error
+  c->cut_short = true;
   c->epoch += 1;
   c->last_stream = st;
   c->launched = true;
@@ -746,6 +749,7 @@ static mk_status launch_shared(mk_ctx* c, const int32_t* tokens, const int32_t* 
     sink.frag_stride = s.Hq / s.Hkv * s.hd + mk::kActPad;
     MK_TRY(mk::ops::prefix_attention(&at, sink, st));
   }
+  c->cut_short = false;
   return MK_OK;
 }
 
@@ -807,7 +811,7 @@ mk_status mk_check(mk_ctx* c, int32_t* device_status, int32_t* detail) {
   if (device_status) *device_status = st[mk::ST_CODE];
   if (detail)
     for (int i = 0; i < 8; ++i) detail[i] = st[i];
-  if (st[mk::ST_CODE] != 0 || st[mk::ST_ABORT] != 0) {
+  if (st[mk::ST_CODE] != 0 || st[mk::ST_ABORT] != 0 || c->cut_short) {
     // a step that stopped part-way leaves counters short of their targets:
     // restart the epochs so the next step begins from a clean state
     MK_CUDA(cudaMemset(c->d_status, 0, sizeof(st)));
@@ -817,7 +821,9 @@ mk_status mk_check(mk_ctx* c, int32_t* device_status, int32_t* detail) {
     if (c->racc.ptr) MK_CUDA(cudaMemset(c->racc.ptr, 0, c->racc.bytes));
     if (c->ssacc.ptr) MK_CUDA(cudaMemset(c->ssacc.ptr, 0, c->ssacc.bytes));
     c->epoch = 0;
-    return st[mk::ST_CODE] != 0 ? (mk_status)st[mk::ST_CODE] : MK_ERR_DEVICE;
+    c->cut_short = false;
+    if (st[mk::ST_CODE] != 0) return (mk_status)st[mk::ST_CODE];
+    return st[mk::ST_ABORT] != 0 ? MK_ERR_DEVICE : MK_OK;   // a failed launch was its call's to report
   }
   return MK_OK;
 }

@@ -62,6 +62,7 @@ static int g_interp = 0, g_append = 0, g_attend = 0, g_sample = 0, g_added = 0;
 static int g_fail_interp = -1, g_fail_append = -1, g_fail_attend = -1, g_fail_sample = -1;
 static uint32_t g_epoch = 0;
 static uint32_t* g_counters = nullptr;
+static std::vector<int> g_touched;   // counters that a shared step adds to ahead of its launches
 static void clear_tally() { g_interp = g_append = g_attend = g_sample = g_added = 0; }
 namespace mk {
 cudaError_t launch_interp(const Params& p, int, cudaStream_t) {
@@ -80,7 +81,11 @@ mk_status sample(const mk_sample_args*, int32_t*, int32_t*, int32_t*, cudaStream
 cudaError_t add_to_counters(uint32_t* c, const int32_t* pairs, int n, cudaStream_t) {
   ++g_added;
   g_counters = c;
-  for (int i = 0; i < n; ++i) c[pairs[2 * i]] += (uint32_t)pairs[2 * i + 1];
+  g_touched.clear();
+  for (int i = 0; i < n; ++i) {
+    c[pairs[2 * i]] += (uint32_t)pairs[2 * i + 1];
+    g_touched.push_back(pairs[2 * i]);
+  }
   return cudaSuccess;
 }
 }  // namespace ops
@@ -143,6 +148,37 @@ CASES = {
   CHECK(g_interp == 0 && g_added == 0 && g_sample == 0 && g_allocs == allocs);
   g_capture = cudaStreamCaptureStatusNone;
   CHECK(shared(c) == MK_OK && g_epoch == 2);
+""",
+    "cut_short": r"""
+  // whichever launch of a shared step fails: nothing runs on the counters that it left short
+  // until mk_check, or a new schedule, has cleared them
+  CHECK(shared(c) == MK_OK);
+  for (int which = 0; which < 8; ++which) {
+    clear_tally();
+    int* fail = which < 3 ? &g_fail_interp : which < 5 ? &g_fail_append : &g_fail_attend;
+    if (which == 7) fail = &g_fail_sample;
+    *fail = which < 3 ? which : which < 5 ? which - 3 : which < 7 ? which - 5 : 0;
+    CHECK(sampled(c, 1) == MK_ERR_CUDA);
+    *fail = -1;
+    const int ran = g_interp + g_append + g_attend + g_added;
+    if (which == 7) {                     // between two steps: both can go on
+      CHECK(step(c) == MK_OK && shared(c) == MK_OK && mk_check(c, nullptr, nullptr) == MK_OK);
+      continue;
+    }
+    CHECK(shared(c) == MK_ERR_STATE && step(c) == MK_ERR_STATE && sampled(c, 0) == MK_ERR_STATE);
+    CHECK(mk_decode_greedy(c, 1, tokens, positions, table, lens, logits, out, nullptr) == MK_ERR_STATE);
+    CHECK(g_interp + g_append + g_attend + g_added == ran && g_sample == 0);
+    if (which % 2) {
+      CHECK(mk_check(c, nullptr, nullptr) == MK_OK);
+    } else {
+      int32_t n[B] = {0, 10, 100};
+      CHECK(mk_build_schedule(c, B, n, nullptr, 8) == MK_OK);
+    }
+    CHECK(!g_touched.empty());
+    for (int i : g_touched) CHECK(g_counters[i] == 0);
+    CHECK((which % 2 ? shared(c) : step(c)) == MK_OK && g_epoch == 1);
+    CHECK(step(c) == MK_OK && g_epoch == 2);
+  }
 """,
 }
 
