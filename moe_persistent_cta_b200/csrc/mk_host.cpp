@@ -767,6 +767,7 @@ mk_status mk_decode_sample(mk_ctx* c, int32_t n_steps, int32_t* tokens, int32_t*
   if (!c || !how) return MK_ERR_INVALID;
   if (n_steps < 0 || (n_steps > 0 && (!out_tokens || !how->u))) return MK_ERR_INVALID;
   if (!c->have_schedule) return MK_ERR_STATE;
+  if (how->n_groups < 0 || how->n_groups > c->B) return MK_ERR_INVALID;
   mk_sample_args a{};
   a.device = c->device;
   a.batch = c->B;

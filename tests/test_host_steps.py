@@ -149,6 +149,17 @@ CASES = {
   g_capture = cudaStreamCaptureStatusNone;
   CHECK(shared(c) == MK_OK && g_epoch == 2);
 """,
+    "refused": r"""
+  // group counts that are no counts, and group arrays that are not there
+  CHECK(sampled(c, -1) == MK_ERR_INVALID && sampled(c, B + 1) == MK_ERR_INVALID && sampled(c, -1, 0) == MK_ERR_INVALID);
+  mk_sampling how{};
+  how.u = u;
+  how.n_groups = 1;
+  CHECK(mk_decode_sample(c, 1, tokens, positions, table, lens, logits, out, &how, nullptr) == MK_ERR_INVALID);
+  CHECK(mk_decode_step_shared(c, tokens, positions, table, lens, 0, starts, prefix, logits, nullptr) == MK_ERR_INVALID);
+  CHECK(mk_decode_step_shared(c, tokens, positions, table, lens, 1, starts, nullptr, logits, nullptr) == MK_ERR_INVALID);
+  CHECK(g_interp == 0 && g_added == 0 && g_sample == 0 && shared(c) == MK_OK);
+""",
     "cut_short": r"""
   // whichever launch of a shared step fails: nothing runs on the counters that it left short
   // until mk_check, or a new schedule, has cleared them
