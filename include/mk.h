@@ -490,7 +490,8 @@ mk_status mk_decode_step_shared(mk_ctx* ctx, const int32_t* tokens, const int32_
 /* Sampled decoding: mk_decode_greedy with mk_sample in the place of the largest
  * logit.  Step i draws with u[i][b], writes the token to out_tokens[i][b] (-1 if
  * there is nothing to draw) and to tokens[b] (then 0), and advances positions[b]
- * and seq_lens[b].  The rules are mk_sample's, the same in every step; those
+ * and seq_lens[b], which must be equal (no prefill groups; else a device-side
+ * fault of MK_OP_SAMPLE).  The rules are mk_sample's, the same in every step; those
  * that are NULL do not apply.  n_groups > 0 runs the steps as
  * mk_decode_step_shared; 0 as mk_decode_step.  Faults surface through mk_check. */
 typedef struct mk_sampling {

@@ -32,3 +32,21 @@ def test_steps_refuse_a_capture():
         assert err <= MAX_ABS and rel <= REL_L2 and (out == 5).all()
     finally:
         r.close()
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_sampled_steps_refuse_prefill_groups(grouped):
+    # two prompt tokens of one sequence: their rows would go on as two sequences
+    r = TinyRig(configs.TINY, [100, 100], seed=5)
+    try:
+        apart = r.table.clone()
+        r.table[1] = r.table[0]
+        kw = dict(group_start=i32([0, 2]), prefix_lens=i32([64])) if grouped else {}
+        out, u = torch.zeros((1, 2), dtype=torch.int32, device=DEV), torch.rand((1, 2), device=DEV)
+        r.dec.sample(1, r.i32(r.tokens), r.i32([100, 101]), r.table.to(DEV), r.i32([100, 100]), r.logits, out, u, **kw)
+        rc, d = r.dec.check()
+        assert rc == mk.MK_ERR_DEVICE and d[1:5] == [mk.MK_OP_SAMPLE, 1, 101, 100]
+        r.dec.sample(1, r.i32(r.tokens), r.i32([100, 100]), apart.to(DEV), r.i32([100, 100]), r.logits, out, u, **kw)
+        r.dec.check_ok()
+    finally:
+        r.close()
