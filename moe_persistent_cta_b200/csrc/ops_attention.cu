@@ -1322,12 +1322,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>, W > 1 ? 1 : 8) join_kernel
         float fi[kAhead], v[kAhead][C];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          fi[u] = __shfl_sync(kFull, f, i1 + u);       // 0 behind the last
-          const float li = __shfl_sync(kFull, ml.y, i1 + u);
+          fi[u] = __shfl_sync(kFull, f, i1 + u);
+          const float li = __shfl_sync(kFull, ml.y, i1 + u);   // 0 behind the last
           const float* src = p.part + __shfl_sync(kFull, (unsigned long long)at_row, i1 + u) * HD + lane * C;
 #pragma unroll
           for (int k = 0; k < C; ++k) v[u][k] = 0.0f;
-          if (fi[u] != 0.0f) {
+          // Any share that saw something counts, however small its weight: NaN and
+          // infinities stay what they are when the weight's exponential is 0.
+          if (li != 0.0f) {
             l = fmaf(li, fi[u], l);
             if constexpr (C == 4) {
               const float4 t = *reinterpret_cast<const float4*>(src);

@@ -160,3 +160,44 @@ def test_status_of_a_captured_call():
             graph.replay()
         rc, detail = status.check()
         assert (rc == mk.MK_OK) if good else (rc == mk.MK_ERR_DEVICE and detail[1] == 1)
+
+
+# ------------------------------------------------- values that are no numbers --
+
+@pytest.mark.parametrize("lens", [(200, 94, 131), (94, 70)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_nan_beside_far_larger_scores(hd, lens):
+    """A key that is NaN in a short remainder shows in the row's result, also where
+    the prefix's scores are so much larger that the remainder's weight is 0; other
+    rows are as if it were not there."""
+    g = gen(11)
+    n, width = len(lens), 4
+    bad = lens.index(94)
+    kp, vp = (torch.randn((n * width, 2, 64, hd), generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((n, 4, hd), generator=g).to(torch.bfloat16)
+    table = torch.randperm(n * width, generator=g).view(n, width).to(torch.int32)
+    for h in range(4):                                   # scores of some hundreds in the prefix
+        kp[int(table[0, 0]), h // 2, 5 + h] = 320.0 / hd ** 0.5 * q[bad, h] / (q[bad, h].float() ** 2).mean() ** 0.5
+    pos = [x - 1 for x in lens]
+    want = ops_oracle.attention(q, kp, vp, table, pos, [0, n], [64], hd ** -0.5)
+    assert want[3][bad].min() > 200
+    kp[int(table[bad, 1]), 1, 7] = math.nan              # token 71 of the entry, in KV head 1
+    lse = torch.zeros((n, 4), device=DEV)
+    out = ops.prefix_attention(q.to(DEV), kp.to(DEV), vp.to(DEV), table.to(DEV), i32(pos), i32([0, n]), i32([64]),
+                               lse=lse).cpu()
+    assert torch.isnan(out[bad, 2:]).all() and torch.isnan(lse[bad, 2:]).all()
+    out[bad, 2:] = want[0][bad, 2:].to(torch.bfloat16)
+    check_attention(out, want)
+
+
+def test_attention_infinite_value_beside_far_larger_scores():
+    # the weight's exponential is 0, the value infinite: no finite result
+    g = gen(12)
+    kp, vp = (torch.randn((4, 1, 64, 64), generator=g).to(torch.float16) for _ in range(2))
+    q = torch.randn((1, 1, 64), generator=g).to(torch.float16)
+    kp[0, 0, 3] = 40.0 * q[0, 0]
+    args = lambda: (q.to(DEV), kp.to(DEV), vp.to(DEV), i32([[0, 1, 2, 3]]), i32([250]), i32([0, 1]), i32([64]))  # noqa: E731
+    assert torch.isfinite(ops.prefix_attention(*args())).all()
+    vp[2, 0, 9, :7] = math.inf
+    out = ops.prefix_attention(*args()).cpu()[0, 0]
+    assert not torch.isfinite(out[:7]).any() and torch.isfinite(out[7:]).all()
