@@ -31,6 +31,7 @@ class Decoder:
         self.shape = dict(shape)
         self.L = shape["n_layers"]
         self.max_batch = max_batch
+        self.device = int(device)
         self.n_pages = int(k_pool.shape[1])
         cfg = mk.make_config(shape, max_batch, self.n_pages)
         L = self.L
@@ -113,10 +114,30 @@ class Decoder:
                                      _ptr(out_tokens), c_void_p(s.cuda_stream))
         mk.check_status(st, "mk_decode_greedy")
 
+    def _holds(self, name: str, t: torch.Tensor, dtype, size: int) -> None:
+        """A tensor that the device reads or writes `size` values of."""
+        if t.dtype != dtype or t.get_device() != self.device:
+            raise TypeError(f"{name} must be a {str(dtype)[6:]} tensor on cuda:{self.device}")
+        if t.numel() < size:
+            raise ValueError(f"{name} holds fewer than {size} values")
+
+    def _step_inputs(self, tokens, positions, page_table, seq_lens, logits) -> None:
+        for name, t in (("tokens", tokens), ("positions", positions), ("seq_lens", seq_lens)):
+            self._holds(name, t, torch.int32, self.batch)
+        if page_table.shape[-1] != self.max_pages:
+            raise ValueError("page_table row length differs from the schedule's")
+        self._holds("page_table", page_table, torch.int32, self.batch * self.max_pages)
+        self._holds("logits", logits, torch.float32, self.batch * self.shape["vocab"])
+
+    def _stream(self, stream):
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if s.device_index != self.device:
+            raise ValueError(f"stream must be of cuda:{self.device}")
+        return s
+
     def _groups(self, group_start: torch.Tensor, prefix_lens: torch.Tensor) -> int:
-        for t in (group_start, prefix_lens):
-            if t.dtype != torch.int32 or not t.is_cuda:
-                raise TypeError("group_start and prefix_lens must be int32 CUDA tensors")
+        self._holds("group_start", group_start, torch.int32, 0)
+        self._holds("prefix_lens", prefix_lens, torch.int32, 0)
         n = prefix_lens.numel()
         if not 1 <= n <= self.batch or group_start.numel() != n + 1:
             raise ValueError("need 1 .. batch prefix lengths and one more group start")
@@ -128,15 +149,9 @@ class Decoder:
         """One step of a batch whose entries share prefixes (mk_decode_step_shared):
         group g is entries group_start[g] .. group_start[g + 1] - 1, whose first
         prefix_lens[g] tokens are read through the first entry's page-table row."""
-        for t in (tokens, positions, page_table, seq_lens):
-            if t.dtype != torch.int32 or not t.is_cuda:
-                raise TypeError("step inputs must be int32 CUDA tensors")
-        if logits.dtype != torch.float32 or not logits.is_cuda:
-            raise TypeError("logits must be a float32 CUDA tensor")
-        if page_table.shape[-1] != self.max_pages:
-            raise ValueError("page_table row length differs from the schedule's")
+        self._step_inputs(tokens, positions, page_table, seq_lens, logits)
         n = self._groups(group_start, prefix_lens)
-        s = stream if stream is not None else torch.cuda.current_stream()
+        s = self._stream(stream)
         st = mk.lib.mk_decode_step_shared(
             self._ctx, _ptr(tokens), _ptr(positions), _ptr(page_table), _ptr(seq_lens), n,
             _ptr(group_start), _ptr(prefix_lens), _ptr(logits), c_void_p(s.cuda_stream))
@@ -155,15 +170,8 @@ class Decoder:
         ``ops.sample``; with group_start and prefix_lens the steps are those of
         ``step_shared``.  logprobs, if given, receives n_steps x batch
         log-probabilities.  Asynchronous."""
-        for t in (tokens, positions, page_table, seq_lens, out_tokens):
-            if t.dtype != torch.int32 or not t.is_cuda:
-                raise TypeError("sampling inputs and outputs must be int32 CUDA tensors")
-        if logits.dtype != torch.float32 or not logits.is_cuda:
-            raise TypeError("logits must be a float32 CUDA tensor")
-        if page_table.shape[-1] != self.max_pages:
-            raise ValueError("page_table row length differs from the schedule's")
-        if out_tokens.numel() < n_steps * self.batch:
-            raise ValueError("out_tokens holds fewer than n_steps x batch tokens")
+        self._step_inputs(tokens, positions, page_table, seq_lens, logits)
+        self._holds("out_tokens", out_tokens, torch.int32, n_steps * self.batch)
         how = mk.mk_sampling()
         for name, t, dtype, size in (
                 ("u", u, torch.float32, n_steps * self.batch),
@@ -174,17 +182,14 @@ class Decoder:
                 ("logprobs", logprobs, torch.float32, n_steps * self.batch)):
             if t is None:
                 continue
-            if t.dtype != dtype or not t.is_cuda:
-                raise TypeError(f"{name} must be a {str(dtype)[6:]} CUDA tensor")
-            if t.numel() < size:
-                raise ValueError(f"{name} holds fewer than {size} values")
+            self._holds(name, t, dtype, size)
             setattr(how, name, _ptr(t))
         if (group_start is None) != (prefix_lens is None):
             raise ValueError("group_start and prefix_lens go together")
         if group_start is not None:
             how.n_groups = self._groups(group_start, prefix_lens)
             how.group_start, how.prefix_lens = _ptr(group_start), _ptr(prefix_lens)
-        s = stream if stream is not None else torch.cuda.current_stream()
+        s = self._stream(stream)
         st = mk.lib.mk_decode_sample(self._ctx, int(n_steps), _ptr(tokens), _ptr(positions),
                                      _ptr(page_table), _ptr(seq_lens), _ptr(logits),
                                      _ptr(out_tokens), byref(how), c_void_p(s.cuda_stream))

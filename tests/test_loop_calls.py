@@ -1,0 +1,99 @@
+"""Refusals of the decode loop's Python functions, without a GPU: tensors that do
+not fit the schedule are refused before the library is called."""
+
+import pytest
+import torch
+
+from moe_persistent_cta_b200 import engine, mk
+
+B, PAGES, V = 3, 4, 50
+
+
+class OnDevice:
+    """What the checks look at of a tensor on a device."""
+
+    def __init__(self, *shape, dtype=torch.int32, device=0):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, device
+
+    def get_device(self):
+        return self.device
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+class Stream:
+    cuda_stream, device_index = 0, 0
+
+
+def decoder():
+    d = engine.Decoder.__new__(engine.Decoder)
+    d.shape, d.batch, d.max_pages, d.device, d._ctx = dict(vocab=V), B, PAGES, 0, None
+    return d
+
+
+F32 = torch.float32
+
+
+def inputs(**kw):
+    d = dict(tokens=OnDevice(B), positions=OnDevice(B), page_table=OnDevice(B, PAGES), seq_lens=OnDevice(B),
+             logits=OnDevice(B, V, dtype=F32), group_start=OnDevice(3), prefix_lens=OnDevice(2), stream=Stream())
+    d.update(kw)
+    return d
+
+
+def sample_inputs(**kw):
+    return inputs(n_steps=2, out_tokens=OnDevice(2, B), u=OnDevice(2, B, dtype=F32), **kw)
+
+
+BAD_STEP = [
+    (ValueError, dict(tokens=OnDevice(B - 1))), (ValueError, dict(positions=OnDevice(B - 1))),
+    (ValueError, dict(seq_lens=OnDevice(1))), (ValueError, dict(page_table=OnDevice(B - 1, PAGES))),
+    (ValueError, dict(page_table=OnDevice(B, PAGES + 1))), (ValueError, dict(logits=OnDevice(B, V - 1, dtype=F32))),
+    (ValueError, dict(group_start=OnDevice(2))), (ValueError, dict(prefix_lens=OnDevice(0), group_start=OnDevice(1))),
+    (ValueError, dict(prefix_lens=OnDevice(B + 1), group_start=OnDevice(B + 2))),
+    (TypeError, dict(tokens=OnDevice(B, dtype=torch.int64))), (TypeError, dict(seq_lens=OnDevice(B, device=-1))),
+    (TypeError, dict(positions=OnDevice(B, device=1))), (TypeError, dict(logits=OnDevice(B, V, dtype=torch.float16))),
+    (TypeError, dict(page_table=OnDevice(B, PAGES, device=1))), (TypeError, dict(prefix_lens=OnDevice(2, device=1))),
+]
+BAD_SAMPLE = [
+    (ValueError, dict(out_tokens=OnDevice(2 * B - 1))), (ValueError, dict(u=OnDevice(B, dtype=F32))),
+    (ValueError, dict(temperature=OnDevice(B - 1, dtype=F32))), (ValueError, dict(logprobs=OnDevice(B, dtype=F32))),
+    (ValueError, dict(group_start=None)), (TypeError, dict(top_k=OnDevice(B, dtype=F32))),
+    (TypeError, dict(top_p=OnDevice(B, dtype=F32, device=1))), (TypeError, dict(out_tokens=OnDevice(2, B, device=1))),
+]
+
+
+@pytest.mark.parametrize("error,kw", BAD_STEP)
+def test_step_shared_refusals(error, kw):
+    with pytest.raises(error):
+        decoder().step_shared(**inputs(**kw))
+
+
+@pytest.mark.parametrize("error,kw", BAD_STEP + BAD_SAMPLE)
+def test_sample_refusals(error, kw):
+    with pytest.raises(error):
+        decoder().sample(**{**sample_inputs(), **kw})
+
+
+def test_streams_of_another_device_are_refused():
+    other = Stream()
+    other.device_index = 1
+    with pytest.raises(ValueError):
+        decoder().step_shared(**inputs(stream=other))
+    with pytest.raises(ValueError):
+        decoder().sample(**sample_inputs(stream=other))
+
+
+def test_fitting_tensors_reach_the_library():
+    # which has no context here
+    for call in (lambda: decoder().step_shared(**inputs()), lambda: decoder().sample(**sample_inputs())):
+        with pytest.raises(mk.MKError) as e:
+            call()
+        assert e.value.status == mk.MK_ERR_INVALID
