@@ -58,6 +58,8 @@ class Decoder:
         t.k_pool = arr([k_pool[l] for l in range(L)])
         t.v_pool = arr([v_pool[l] for l in range(L)])
         self._inv_freq = None                       # of append_kv
+        self._append_status = ops.Status(k_pool.device)
+        self._appended = False                      # some call names that word
         self._tensors = (weights, k_pool, v_pool)   # keep caller tensors alive
         ctx = c_void_p()
         mk.check_status(mk.lib.mk_create(byref(cfg), byref(t), int(device), byref(ctx)),
@@ -202,19 +204,27 @@ class Decoder:
         that the steps read (``ops.rope_append``): a prompt that was computed
         outside the step, handed over in one piece.  k and v are [tokens][kv
         heads][head size] before the rotation; the other arguments are
-        ``ops.rope_append``'s."""
+        ``ops.rope_append``'s.  Without a ``status`` of its own, a call's fault is
+        the decoder's: the next ``check`` reports it."""
         _, k_pool, v_pool = self._tensors
         if self._inv_freq is None:
             self._inv_freq, _ = ops.rope_frequencies(
                 self.shape["head_dim"], self.shape.get("rope_theta", 1.0e4), device=k_pool.device)
+        if status is None:
+            status, self._appended = self._append_status, True
         ops.rope_append(None, k, v, positions, page_table, k_pool[layer], v_pool[layer],
                         self._inv_freq, seq=seq, status=status, stream=stream)
 
     def check(self):
-        """Synchronize and return (status, detail list)."""
+        """Synchronize and return (status, detail list): of the steps, and where
+        they are clean of the ``append_kv`` calls since the last check."""
         st = c_int32(0)
         detail = (c_int32 * 8)()
         rc = mk.lib.mk_check(self._ctx, byref(st), detail)
+        if rc == mk.MK_OK and self._appended:
+            rc, where = self._append_status.check()
+            if rc != mk.MK_OK:
+                return rc, [rc] + where + [0] * 3
         return int(rc), [int(v) for v in detail]
 
     def check_ok(self) -> None:

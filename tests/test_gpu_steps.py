@@ -50,3 +50,49 @@ def test_sampled_steps_refuse_prefill_groups(grouped):
         r.dec.check_ok()
     finally:
         r.close()
+
+
+def test_faults_of_append_kv_reach_the_decoder():
+    shape = configs.TINY
+    L, hkv, hd = shape["n_layers"], shape["n_kv_heads"], shape["head_dim"]
+    r = TinyRig(shape, [100], seed=6)
+    try:
+        k = torch.randn((3, hkv, hd), device=DEV)
+        table, seq = r.table.to(DEV), i32([0, 0, 0])
+        r.dec.append_kv(0, k, k, i32([100, 101, 102]), table, seq=seq)
+        r.dec.check_ok()
+        limit = r.table.shape[1] * 64
+        # a position behind the table, a page of the pool that is not there
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)
+        r.dec.append_kv(1, k, k, i32([100, limit, 102]), table, seq=seq, stream=side)
+        rc, d = r.dec.check()
+        assert rc == mk.MK_ERR_DEVICE and d == [rc, mk.MK_OP_ROPE_APPEND, 1, limit, limit, 0, 0, 0]
+        r.dec.check_ok()
+        bad = table.clone()
+        bad[0, 1] = r.n_pages
+        r.dec.append_kv(1, k, k, i32([1, 2, 100]), bad, seq=seq)
+        with pytest.raises(mk.MKError) as e:
+            r.dec.check_ok()
+        assert e.value.detail[1:5] == [mk.MK_OP_ROPE_APPEND, 2, r.n_pages, r.n_pages]
+        # a status of the caller's keeps it from the decoder
+        own = ops.Status(DEV)
+        r.dec.append_kv(1, k, k, i32([1, 2, 100]), bad, seq=seq, status=own)
+        r.dec.check_ok()
+        assert own.check()[0] == mk.MK_ERR_DEVICE
+        # a fault of a step comes first, then that of the append
+        r.dec.append_kv(1, k, k, i32([1, 2, 100]), bad, seq=seq)
+        r.dec.step(r.i32(r.tokens), r.i32([100]), bad, r.i32([100]), r.logits)
+        rc, d = r.dec.check()
+        assert rc == mk.MK_ERR_DEVICE
+        rc, d = r.dec.check()
+        assert rc == mk.MK_ERR_DEVICE and d[1] == mk.MK_OP_ROPE_APPEND
+        ref = r.oracle_step()
+        r.kd.copy_(r.k)
+        r.vd.copy_(r.v)
+        err, rel = compare_logits(r.step(), ref)
+        assert err <= MAX_ABS and rel <= REL_L2
+    finally:
+        r.close()
