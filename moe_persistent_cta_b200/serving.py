@@ -190,6 +190,10 @@ def sample_prompt(dec, k_pool: torch.Tensor, v_pool: torch.Tensor, pool: PagePoo
     and their log-probabilities, [steps][samples], and the last logits."""
     dev = k_pool.device
     n = len(tokens)
+    if n != dec.batch:
+        raise ValueError(f"the schedule is built for {dec.batch} entries, not {n}")
+    if prompt_len < 0 or steps < 0:
+        raise ValueError("prompt_len and steps must not be negative")
     whole, rest = divmod(prompt_len, PAGE)
     if len(prompt_pages) < pages_for(prompt_len):
         raise ValueError("prompt_pages does not hold prompt_len tokens")
@@ -224,9 +228,9 @@ def sample_prompt(dec, k_pool: torch.Tensor, v_pool: torch.Tensor, pool: PagePoo
                        group_start=torch.tensor([0, n], **i32),
                        prefix_lens=torch.tensor([whole * PAGE], **i32), stream=s,
                        **sampling_rules(sampling or {}, n, dev))
-        s.synchronize()
         dec.check_ok()
     finally:
+        s.synchronize()               # no step writes the pages any more, however far it came
         for pages in own:
             pool.release(pages)
     return {"tokens": out.cpu().numpy(), "logprobs": logprobs.cpu().numpy(), "logits": logits}

@@ -4,7 +4,7 @@ not fit the schedule are refused before the library is called."""
 import pytest
 import torch
 
-from moe_persistent_cta_b200 import engine, mk
+from moe_persistent_cta_b200 import engine, mk, serving
 
 B, PAGES, V = 3, 4, 50
 
@@ -97,3 +97,18 @@ def test_fitting_tensors_reach_the_library():
         with pytest.raises(mk.MKError) as e:
             call()
         assert e.value.status == mk.MK_ERR_INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(tokens=[1, 2]), dict(tokens=[1, 2, 3, 4]), dict(tokens=[]), dict(steps=-1),
+                                dict(prompt_len=-1), dict(prompt_len=129), dict(steps=64 * PAGES - 63)])
+def test_sample_prompt_refusals(kw):
+    # samples that are not the schedule's, a prompt longer than its pages, more tokens than the table
+    # holds; the pool keeps its pages
+    pool = serving.PagePool(20)
+    pages = pool.alloc(2)
+    k = torch.zeros((1, 20, 1, 64, 64), dtype=torch.bfloat16)
+    args = dict(prompt_len=64, tokens=[1, 2, 3], steps=2)
+    args.update(kw)
+    with pytest.raises(ValueError):
+        serving.sample_prompt(decoder(), k, k, pool, pages, max_pages_per_seq=PAGES, **args)
+    assert pool.free_count() == 18
