@@ -262,12 +262,13 @@ def run_continuous(dec, shape: Dict, k_pool: torch.Tensor, v_pool: torch.Tensor,
                           max_new, horizon=horizon)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     i32 = dict(dtype=torch.int32, device=dev)
-    tokens = torch.zeros(slots, **i32)
-    lens_d = torch.zeros(slots, **i32)
-    table_d = torch.zeros((slots, max_pages_per_seq), **i32)
-    out = torch.full((steps, slots), -1, **i32)
-    logits = torch.empty((slots, shape["vocab"]), dtype=torch.float32, device=dev)
-    rules = sampling_rules(sampling, slots, dev) if sampling is not None else None
+    with torch.cuda.stream(s):
+        tokens = torch.zeros(slots, **i32)
+        lens_d = torch.zeros(slots, **i32)
+        table_d = torch.zeros((slots, max_pages_per_seq), **i32)
+        out = torch.full((steps, slots), -1, **i32)
+        logits = torch.empty((slots, shape["vocab"]), dtype=torch.float32, device=dev)
+        rules = sampling_rules(sampling, slots, dev) if sampling is not None else None
     gen_u = torch.Generator(device=dev).manual_seed(seed + 1)
     ev = []            # (kind, start event, end event)
     t_rebuild = 0.0

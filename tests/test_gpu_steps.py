@@ -96,3 +96,28 @@ def test_faults_of_append_kv_reach_the_decoder():
         assert err <= MAX_ABS and rel <= REL_L2
     finally:
         r.close()
+
+
+def test_continuous_batching_on_another_stream_than_the_current_one():
+    """What the run makes for itself is made on its stream: a current stream that
+    is behind its work neither delays the rules nor clears the tokens late."""
+    shape = configs.TINY
+    slots, steps, max_pages = 3, 12, 8
+    W = to_dev(synth.make_weights(shape, 0, "cpu"), DEV)
+    kshape = (shape["n_layers"], 3 * slots * max_pages, shape["n_kv_heads"], 64, shape["head_dim"])
+    common = dict(slots=slots, steps=steps, seed=21, start_lo=5, start_hi=250, mean_new=6, max_new=steps,
+                  max_pages_per_seq=max_pages, sampling=dict(temperature=2.0, top_k=40, top_p=0.95, min_p=0.001))
+    runs = []
+    side = torch.cuda.Stream()
+    for stream in (None, side, side):
+        k, v = (torch.zeros(kshape, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        dec = engine.Decoder(shape, W, k, v, max_batch=slots)
+        try:
+            torch.cuda.synchronize()
+            if stream is not None:
+                torch.cuda._sleep(400_000_000)
+            runs.append(serving.run_continuous(dec, shape, k, v, stream=stream, **common)["tokens"])
+            torch.cuda.synchronize()
+        finally:
+            dec.close()
+    assert np.array_equal(runs[0], runs[1]) and np.array_equal(runs[0], runs[2])
