@@ -188,7 +188,9 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
     int32[tokens], each token's row (-1: padding, left out), or None: token t
     is row t.  inv_freq float64[rotary_dim / 2] and magnitude as from
     ``rope_frequencies``.  Returns q_out ([tokens][query heads][hd] of the
-    pools' type; allocated if None, may be q itself), None without queries."""
+    pools' type; allocated if None, may be q itself), None without queries.  Rows
+    of padding, and of tokens whose place is at fault, are left as they were:
+    zero in a q_out that is allocated here (one that is passed saves the clearing)."""
     dev = _cuda(k, "k")
     handle = _stream(stream, dev)
     pool, n_pages, hkv, hd = _pools(k_pool, v_pool, dev)
@@ -213,7 +215,7 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
         if t and qs[2] != 1:
             raise ValueError("the columns of q must be adjacent")
         if q_out is None:
-            q_out = _output(torch.empty, (t, hq, hd), pool, q.device, stream)
+            q_out = _output(torch.zeros, (t, hq, hd), pool, q.device, stream)
         elif (q_out.shape != shape or not q_out.is_contiguous() or q_out.dtype is not pool
               or q_out.get_device() != dev):
             raise ValueError("q_out must be contiguous, shaped like q and of the pools' type and device")

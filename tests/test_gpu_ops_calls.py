@@ -201,3 +201,32 @@ def test_attention_infinite_value_beside_far_larger_scores():
     vp[2, 0, 9, :7] = math.inf
     out = ops.prefix_attention(*args()).cpu()[0, 0]
     assert not torch.isfinite(out[:7]).any() and torch.isfinite(out[7:]).all()
+
+
+# ---------------------------------------------------- rows that are left out --
+
+def test_queries_of_padding_are_zero_in_an_allocated_output():
+    x = torch.randn((6, 4, 64), generator=gen(13)).to(torch.bfloat16).to(DEV)
+    pool = torch.zeros((2, 1, 64, 64), dtype=torch.bfloat16, device=DEV)
+    freq = ops.rope_frequencies(64, device=DEV)[0]
+    status = ops.Status(DEV)
+    want = torch.zeros((6, 2, 64), dtype=torch.bfloat16, device=DEV)
+    for kept, seq, pos in ((range(6), [0] * 6, range(6)), ([0, 2, 3], [0, -1, 0, 0, -1, -1], range(6)),
+                           ([1], [0, 0, 9, 0, -1, 0], [-1, 1, 2, 128, 4, 200])):
+        stale = torch.full((6, 2, 64), math.nan, dtype=torch.bfloat16, device=DEV)
+        del stale                                        # the allocator hands its memory out next
+        got = ops.rope_append(x[:, :2], x[:, 2:3], x[:, 3:], i32(pos), i32([[0, 1]]), pool, pool.clone(), freq,
+                              seq=i32(seq), status=status)
+        kept = list(kept)
+        if len(kept) == 6:
+            want, all_rows = torch.zeros_like(want), got
+            continue
+        expect = torch.zeros_like(want)
+        expect[kept] = all_rows[kept]
+        assert torch.equal(got, expect)
+        # a q_out that is passed keeps what it held there
+        mine = torch.full_like(want, 5.0)
+        ops.rope_append(x[:, :2], x[:, 2:3], x[:, 3:], i32(pos), i32([[0, 1]]), pool, pool.clone(), freq,
+                        seq=i32(seq), q_out=mine, status=status)
+        rest = [t for t in range(6) if t not in kept]
+        assert torch.equal(mine[kept], expect[kept]) and (mine[rest] == 5.0).all()
