@@ -352,7 +352,8 @@ enum mk_op_id { MK_OP_ROPE_APPEND = 1, MK_OP_PREFIX_ATTENTION = 2, MK_OP_SAMPLE 
  * `magnitude`; columns from rotary_dim (even, 0 .. head_dim) on are copied.
  * Scaled frequencies for stretched contexts are the caller's inv_freq.
  * A sequence's row, position or page out of range is a device-side fault.
- * Two tokens with the same sequence and position leave either one's rows.
+ * Two tokens with the same sequence and position are not detected: pieces of
+ * either one's rows are left.
  * q_out and the pools are 16-byte aligned.                                  */
 typedef struct mk_rope_append_args {
   int32_t device;

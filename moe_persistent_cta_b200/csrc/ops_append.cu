@@ -30,6 +30,7 @@ constexpr int kThreads = 32 * kWarps;
 struct AppendParams {
   int T, rows, max_pages, n_pages, Hq, Hkv, R;
   int splits, rounds;        // warps of a token, and how many times each turns the heads it can at once
+  int blocks;
   float magnitude;
   const void *q, *k, *v;
   long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;   // strides in elements
@@ -222,17 +223,21 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
   }
 }
 
+// A warp takes all heads of a token, as far as its registers hold them; while
+// that gives the device fewer warps than it can run, as few as it turns at once.
+// Returns the number of blocks.
+long long share_out(AppendParams* p, int hd, bool wide_rows) {
+  const int at_once = 32 / (hd / 16), most = wide_rows ? kMostRounds<float> : kMostRounds<__half>;
+  const int rounds = (p->Hq + 2 * p->Hkv + at_once - 1) / at_once;
+  p->splits = (long long)p->T * rounds <= kFewWarps ? rounds : (rounds + most - 1) / most;
+  p->rounds = (rounds + p->splits - 1) / p->splits;
+  return ((long long)p->T * p->splits + kWarps - 1) / kWarps;
+}
+
 template <typename S, typename D, int HD, int MODE, bool WIDE>
-cudaError_t launch(AppendParams p, cudaStream_t stream) {
-  // A warp takes all heads of a token, as far as its registers hold them; while
-  // that gives the device fewer warps than it can run, as few as it turns at once.
-  constexpr int kHeads = 32 / (HD / 16);
-  const int rounds = (p.Hq + 2 * p.Hkv + kHeads - 1) / kHeads;
-  p.splits = (long long)p.T * rounds <= kFewWarps ? rounds : (rounds + kMostRounds<S> - 1) / kMostRounds<S>;
-  p.rounds = (rounds + p.splits - 1) / p.splits;
-  const long long units = (long long)p.T * p.splits;
+cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((units + kWarps - 1) / kWarps));
+  cfg.gridDim = dim3((unsigned)p.blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -240,7 +245,7 @@ cudaError_t launch(AppendParams p, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_append_kernel<S, D, HD, MODE, WIDE>, (const AppendParams)p);
+  return cudaLaunchKernelEx(&cfg, rope_append_kernel<S, D, HD, MODE, WIDE>, p);
 }
 
 template <typename S, typename D, int HD, int MODE>
@@ -292,10 +297,6 @@ extern "C" mk_status mk_rope_append(const mk_rope_append_args* a, void* stream) 
   const size_t es = a->src_type == MK_FP32 ? 4 : 2;
   if (!aligned(a->k, es) || !aligned(a->v, es) || (with_q && !aligned(a->q, es)))
     return MK_ERR_INVALID;
-  DeviceGuard guard(a->device);
-  if (guard.status() != MK_OK) return guard.status();
-  if (a->n_tokens == 0) return MK_OK;
-
   AppendParams p{};
   p.T = a->n_tokens;
   p.rows = a->n_rows;
@@ -304,6 +305,12 @@ extern "C" mk_status mk_rope_append(const mk_rope_append_args* a, void* stream) 
   p.Hq = a->n_q_heads;
   p.Hkv = a->n_kv_heads;
   p.R = a->rotary_dim / 2;
+  const long long blocks = share_out(&p, a->head_dim, es == 4);
+  if (blocks > INT32_MAX) return MK_ERR_CAPACITY;   // of a grid
+  p.blocks = (int)blocks;
+  DeviceGuard guard(a->device);
+  if (guard.status() != MK_OK) return guard.status();
+  if (a->n_tokens == 0) return MK_OK;
   p.magnitude = a->magnitude;
   p.q = a->q; p.k = a->k; p.v = a->v;
   p.q_ts = a->q_token_stride; p.q_hs = a->q_head_stride;
