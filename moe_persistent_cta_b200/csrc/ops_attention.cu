@@ -49,6 +49,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "ops_common.cuh"
@@ -106,7 +107,7 @@ struct AttnParams {
   float* part;
   float2* part_ml;
   Entry* entries;                    // [B], and the line's length behind them
-  int n_slots;
+  int n_slots, slot_rows;            // split shares, and the rows that one can hold
   const void *q, *k_pool, *v_pool;   // for rows computed alone
   long long q_stride;
   void* out;
@@ -117,7 +118,7 @@ struct AttnParams {
 
 // Row of `part` that holds a share of a whole unit.
 __device__ __forceinline__ size_t whole_row(const AttnParams& p, int kind, int stream, int b, int hq) {
-  return (size_t)p.n_slots * 2 * kRows + (((size_t)kind * 2 + stream) * p.B + b) * p.Hq + hq;
+  return (size_t)p.n_slots * 2 * p.slot_rows + (((size_t)kind * 2 + stream) * p.B + b) * p.Hq + hq;
 }
 
 // A block's share of a unit.  Consecutive items whose rows share O make a run.
@@ -1147,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* dst = nullptr;
             if (slot != -2) {
               const int hq = q.head * p.G + r % p.G;
-              const size_t row = slot >= 0 ? ((size_t)slot * 2 + st) * kRows + r
+              const size_t row = slot >= 0 ? ((size_t)slot * 2 + st) * p.slot_rows + r
                                            : whole_row(p, own ? 1 : 0, dual ? 0 : st, q.b0 + e, hq);
               dst = p.part + row * HD;
               // without a step of its own the stream has seen nothing, and O is not its
@@ -1302,7 +1303,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>, W > 1 ? 1 : 8) join_kernel
       float2 ml = make_float2(0.0f, 0.0f);
       if (x < n) {
         at_row = whole ? whole_row(p, kind, dual ? 0 : stream, b, hq)
-                       : ((size_t)(2 * c + (c == c0 ? 1 : 0)) * 2 + stream) * kRows + r;
+                       : ((size_t)(2 * c + (c == c0 ? 1 : 0)) * 2 + stream) * p.slot_rows + r;
         ml = p.part_ml[at_row];
       }
       // a share that saw nothing has no weight, and its O is not looked at
@@ -1439,9 +1440,14 @@ constexpr int kMaxBlocks = 160;      // at least the device's multiprocessors
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// Rows of a split share: a stream's, or as many as the whole batch has.
+int slot_rows(const mk_prefix_attention_args* a) {
+  return std::min(kRows, a->batch * (a->n_q_heads / a->n_kv_heads));
+}
+
 // Split shares: two per block and stream; whole units: two kinds and streams.
 size_t part_rows(const mk_prefix_attention_args* a) {
-  return (size_t)2 * kMaxBlocks * 2 * kRows + (size_t)4 * a->batch * a->n_q_heads;
+  return (size_t)2 * kMaxBlocks * 2 * slot_rows(a) + (size_t)4 * a->batch * a->n_q_heads;
 }
 
 mk_status validate(const mk_prefix_attention_args* a) {
@@ -1559,6 +1565,7 @@ mk_status prefix_attention(const mk_prefix_attention_args* a, const StepSink& si
   p.v_pool = a->v_pool;
   p.q_stride = a->batch > 1 ? a->q_token_stride : row;
   p.n_slots = 2 * kMaxBlocks;
+  p.slot_rows = slot_rows(a);
   p.out = a->out;
   p.lse = a->lse;
   p.sink = sink;

@@ -2,6 +2,7 @@
 streams than the current one, outputs that the functions allocate, status words,
 workspaces and waits that run out."""
 
+import ctypes
 import math
 
 import pytest
@@ -230,3 +231,41 @@ def test_queries_of_padding_are_zero_in_an_allocated_output():
                         seq=i32(seq), q_out=mine, status=status)
         rest = [t for t in range(6) if t not in kept]
         assert torch.equal(mine[kept], expect[kept]) and (mine[rest] == 5.0).all()
+
+
+# -------------------------------------------------------------- workspaces --
+
+@pytest.mark.parametrize("lens,hq,hkv,prefix", [
+    ((20000,), 4, 1, 20000), ((20000,), 2, 2, 0), ((9000, 9100), 3, 1, 8000), ((700, 650, 9), 8, 2, 600),
+    (tuple(range(300, 300 + 40)), 4, 1, 256)])
+def test_attention_stays_inside_its_workspace(lens, hq, hkv, prefix):
+    """A workspace of just the size asked for, in the midst of other memory, at
+    batches of few rows (whose shares are small) and of more rows than a tile's."""
+    b, hd = len(lens), 64
+    g = gen(14)
+    width = max(lens) // 64 + 1
+    kp, vp = (torch.randn((b * width, hkv, 64, hd), generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((b, hq, hd), generator=g).to(torch.bfloat16)
+    table = torch.randperm(b * width, generator=g).view(b, width).to(torch.int32)
+    pos = [n - 1 for n in lens]
+    dev = [x.to(DEV) for x in (q, kp, vp, table)] + [i32(pos), i32([0, b]), i32([prefix])]
+    want = ops.prefix_attention(*dev)
+    a = mk.mk_prefix_attention_args()
+    out = torch.zeros_like(dev[0])
+    for name, value in dict(device=0, batch=b, n_groups=1, max_pages=width, n_pages=b * width, n_q_heads=hq,
+                            n_kv_heads=hkv, head_dim=hd, type=mk.MK_BF16, scale=hd ** -0.5, q_token_stride=hq * hd,
+                            q=dev[0].data_ptr(), k_pool=dev[1].data_ptr(), v_pool=dev[2].data_ptr(),
+                            page_table=dev[3].data_ptr(), positions=dev[4].data_ptr(), group_start=dev[5].data_ptr(),
+                            prefix_lens=dev[6].data_ptr(), out=out.data_ptr()).items():
+        setattr(a, name, value)
+    size, edge = mk.lib.mk_prefix_attention_workspace(ctypes.byref(a)), 1 << 20
+    for fill in (0, 255):
+        memory = torch.full((size + 2 * edge,), fill, dtype=torch.uint8, device=DEV)
+        assert memory.data_ptr() % 256 == 0
+        a.workspace, a.workspace_bytes = memory.data_ptr() + edge, size
+        assert mk.lib.mk_prefix_attention(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == mk.MK_OK
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert (memory[:edge] == fill).all() and (memory[edge + size:] == fill).all()
+        a.workspace_bytes = size - 1
+        assert mk.lib.mk_prefix_attention(ctypes.byref(a), None) == mk.MK_ERR_CAPACITY
