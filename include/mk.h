@@ -322,10 +322,11 @@ mk_status mk_plan_schedule(const mk_config* cfg, int n_ctas, int batch,
  *    stream; the caller's current device is put back before the call returns.
  *  - `status` is NULL or a device int32[8] that the caller zeroed: the first
  *    device-side fault of any call that names it is latched there as {code,
- *    operator, entry, value, limit} with code MK_ERR_DEVICE (MK_ERR_TIMEOUT if a
- *    device-side wait ran out: the call's output is then unusable); the
- *    operator numbers are those of mk_op_id.  Faulty entries are left out,
- *    the others are computed.
+ *    operator, entry, value, limit} with code MK_ERR_DEVICE, or MK_ERR_TIMEOUT
+ *    if a device-side wait of mk_prefix_attention ran out (about half a second;
+ *    `entry` is then the block; the rows concerned are computed again without
+ *    waits, slowly); the operator numbers are those of mk_op_id.  Faulty entries
+ *    are left out, the others are computed.
  *  - Nothing is allocated and nothing is kept between calls, so calls may
  *    overlap on different streams and be captured into graphs, as long as
  *    their output and workspace memory does not overlap.                    */
@@ -422,6 +423,13 @@ typedef struct mk_prefix_attention_args {
 } mk_prefix_attention_args;
 size_t mk_prefix_attention_workspace(const mk_prefix_attention_args* args);
 mk_status mk_prefix_attention(const mk_prefix_attention_args* args, void* stream);
+
+/* Failure-detection self-test: mk_prefix_attention with one block whose keys and
+ * values never arrive.  That block's waits run out by design after half a second
+ * (no fault, no unbounded spin): `status`, which must not be NULL, receives
+ * {MK_ERR_TIMEOUT, MK_OP_PREFIX_ATTENTION, 0, ..}, and out and lse are complete all
+ * the same.  Asynchronous like mk_prefix_attention.                          */
+mk_status mk_prefix_attention_selftest(const mk_prefix_attention_args* args, void* stream);
 
 /* Draw one token per row of logits from given uniform numbers.
  *   logits      [batch] rows of `vocab` elements of `type`, row_stride apart

@@ -70,9 +70,11 @@ constexpr int kMaxBatch = 4096;
 constexpr int kMaxGroup = 64;        // query heads per KV head
 constexpr float kRescale = 8.0f;     // log2 of the growth that O may lag behind
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kWaitCycles = 1 << 30; // about half a second at any clock
+// Limit of a wait: about half a second at any clock.  (As an argument of the
+// launch it cost 1 % of a long call, by the compiler's order of things alone.)
+constexpr int kWaitCycles = 1 << 30;
 
-// What the joining launch needs of an entry, written by block 0: the places
+// What the joining launch needs of an entry, written by the last block: the places
 // in the line of its unit's first prefix tile and of its first own tile for KV
 // head 0, how far the next head's are, and how many tiles there are.
 struct __align__(16) Entry {
@@ -106,7 +108,10 @@ struct AttnParams {
   // of whole ones (prefix, then own tokens)
   float* part;
   float2* part_ml;
-  Entry* entries;                    // [B], and the line's length behind them
+  Entry* entries;                    // [B]
+  int* line_total;                   // the line's length
+  int* gave_up;                      // [block]: a wait ran out, and its shares are not complete
+  int stall;                         // block whose tiles never arrive (the self-test), or -1
   int n_slots, slot_rows;            // split shares, and the rows that one can hold
   const void *q, *k_pool, *v_pool;   // for rows computed alone
   long long q_stride;
@@ -546,7 +551,7 @@ __device__ int list_items(Block& s, const AttnParams& p, int32_t* tmp, int skip,
   const Line line(own0 + p.Hkv * total[2], p.grid);
   auto chunk_of = [&](int b) { return b / p.MB * p.MB; };
   if (teller) {
-    if (threadIdx.x == 0) reinterpret_cast<int*>(p.entries + B)[0] = line.total;
+    if (threadIdx.x == 0) *p.line_total = line.total;
     for (int b = threadIdx.x; b < B; b += kThreads) {
       const int g = group[b], cf = chunk_of(b), ce = min(B, cf + p.MB);
       Entry e{};
@@ -827,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t st = ring % L::kStages, bar = b_full + 8 * st;
         if (ring >= L::kStages) ok = ok && wait(s, b_empty + 8 * st, (ring / L::kStages - 1) & 1, p);
         ok = __all_sync(kFull, ok);
-        if (ok && lane == 0) {
+        if (ok && lane == 0 && (int)blockIdx.x != p.stall) {
           if (!both) mbar_arrive(b_empty + 8 * st);
           mbar_expect(bar, L::kTileBytes);
           const uint32_t dst = sb + L::kRing + st * L::kTileBytes;
@@ -1183,7 +1188,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // A wait that ran out may have left copies and MMAs in flight: give them time.
-  if (*(volatile int*)&s.abort) {
+  // The block's shares are then not looked at.
+  const bool gave_up = *(volatile int*)&s.abort != 0;
+  if (threadIdx.x == 0) p.gave_up[blockIdx.x] = gave_up;
+  if (gave_up) {
     const long long t0 = clock64();
     while (clock64() - t0 < 20000000) {
     }
@@ -1279,7 +1287,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>, W > 1 ? 1 : 8) join_kernel
     }
     return;
   }
-  const Line line(reinterpret_cast<const int*>(p.entries + p.B)[0], p.grid);
+  const Line line(*p.line_total, p.grid);
   float acc[C], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int i = 0; i < C; ++i) acc[i] = 0.0f;
@@ -1305,6 +1313,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>, W > 1 ? 1 : 8) join_kernel
         at_row = whole ? whole_row(p, kind, dual ? 0 : stream, b, hq)
                        : ((size_t)(2 * c + (c == c0 ? 1 : 0)) * 2 + stream) * p.slot_rows + r;
         ml = p.part_ml[at_row];
+        // unfinished: the row's sum is no number, and it is computed alone
+        if (p.gave_up[c]) ml = make_float2(0.0f, __int_as_float(0x7fffffff));
       }
       // a share that saw nothing has no weight, and its O is not looked at
       float top = ml.y == 0.0f ? -INFINITY : ml.x;
@@ -1514,12 +1524,10 @@ size_t workspace_size(const mk_prefix_attention_args* a) {
   if (validate(a) != MK_OK) return 0;
   const size_t rows = part_rows(a);
   return round256(rows * a->head_dim * sizeof(float)) + round256(rows * sizeof(float2)) +
-         round256(sizeof(Entry) * (size_t)a->batch + sizeof(int));
+         round256(sizeof(Entry) * (size_t)a->batch + sizeof(int) * (1 + kMaxBlocks));
 }
 
-}  // namespace
-
-mk_status prefix_attention(const mk_prefix_attention_args* a, const StepSink& sink, cudaStream_t st) {
+mk_status run(const mk_prefix_attention_args* a, const StepSink& sink, cudaStream_t st, int stall) {
   mk_status s = validate(a);
   if (s != MK_OK) return s;
   if (a->batch == 0 || a->n_groups == 0) return MK_OK;
@@ -1559,6 +1567,9 @@ mk_status prefix_attention(const mk_prefix_attention_args* a, const StepSink& si
   p.part_ml = reinterpret_cast<float2*>(w);
   w += round256(rows * sizeof(float2));
   p.entries = reinterpret_cast<Entry*>(w);
+  p.line_total = reinterpret_cast<int*>(p.entries + a->batch);
+  p.gave_up = p.line_total + 1;
+  p.stall = stall;
   p.grid = blocks;
   p.q = a->q;
   p.k_pool = a->k_pool;
@@ -1603,11 +1614,22 @@ mk_status prefix_attention(const mk_prefix_attention_args* a, const StepSink& si
   return from_cuda(e);
 }
 
+}  // namespace
+
+mk_status prefix_attention(const mk_prefix_attention_args* a, const StepSink& sink, cudaStream_t st) {
+  return run(a, sink, st, -1);
+}
+
 }  // namespace ops
 }  // namespace mk
 
 extern "C" size_t mk_prefix_attention_workspace(const mk_prefix_attention_args* args) {
   return mk::ops::workspace_size(args);
+}
+
+extern "C" mk_status mk_prefix_attention_selftest(const mk_prefix_attention_args* args, void* stream) {
+  if (!args || !args->status) return MK_ERR_INVALID;
+  return mk::ops::run(args, mk::ops::StepSink{}, static_cast<cudaStream_t>(stream), 0);
 }
 
 extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* args, void* stream) {

@@ -33,7 +33,8 @@ EXPORTS = (
     "mk_check", "mk_selftest_timeout", "mk_set_timeout_ms", "mk_set_trace", "mk_debug_read",
     "mk_debug_size",
     "mk_plan_schedule", "mk_rope_append", "mk_prefix_attention_workspace",
-    "mk_prefix_attention", "mk_sample", "mk_decode_step_shared", "mk_decode_sample",
+    "mk_prefix_attention", "mk_prefix_attention_selftest", "mk_sample", "mk_decode_step_shared",
+    "mk_decode_sample",
     "mk_strerror", "mk_destroy",
 )
 
@@ -127,6 +128,7 @@ def _load():
         "mk_rope_append": (c_int, [c_void_p, c_void_p]),
         "mk_prefix_attention_workspace": (c_size_t, [c_void_p]),
         "mk_prefix_attention": (c_int, [c_void_p, c_void_p]),
+        "mk_prefix_attention_selftest": (c_int, [c_void_p, c_void_p]),
         "mk_sample": (c_int, [c_void_p, c_void_p]),
         "mk_decode_step_shared": (c_int, [c_void_p] + [c_void_p] * 4 + [c_int32] + [c_void_p] * 4),
         "mk_decode_sample": (c_int, [c_void_p, c_int32] + [c_void_p] * 6 +

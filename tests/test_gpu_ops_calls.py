@@ -235,6 +235,21 @@ def test_queries_of_padding_are_zero_in_an_allocated_output():
 
 # -------------------------------------------------------------- workspaces --
 
+def c_arguments(args, out, **more):
+    """mk_prefix_attention_args of prefix_attention's tensors (no workspace)."""
+    q, kp, vp, table, pos, start, prefix = args
+    a = mk.mk_prefix_attention_args()
+    d = dict(device=0, batch=q.shape[0], n_groups=prefix.numel(), max_pages=table.shape[1], n_pages=kp.shape[0],
+             n_q_heads=q.shape[1], n_kv_heads=kp.shape[1], head_dim=q.shape[2],
+             type=mk.MK_BF16 if q.dtype is torch.bfloat16 else mk.MK_FP16, scale=q.shape[2] ** -0.5,
+             q_token_stride=q.stride(0), q=q.data_ptr(), k_pool=kp.data_ptr(), v_pool=vp.data_ptr(),
+             page_table=table.data_ptr(), positions=pos.data_ptr(), group_start=start.data_ptr(),
+             prefix_lens=prefix.data_ptr(), out=out.data_ptr(), **more)
+    for name, value in d.items():
+        setattr(a, name, value)
+    return a
+
+
 @pytest.mark.parametrize("lens,hq,hkv,prefix", [
     ((20000,), 4, 1, 20000), ((20000,), 2, 2, 0), ((9000, 9100), 3, 1, 8000), ((700, 650, 9), 8, 2, 600),
     (tuple(range(300, 300 + 40)), 4, 1, 256)])
@@ -250,14 +265,8 @@ def test_attention_stays_inside_its_workspace(lens, hq, hkv, prefix):
     pos = [n - 1 for n in lens]
     dev = [x.to(DEV) for x in (q, kp, vp, table)] + [i32(pos), i32([0, b]), i32([prefix])]
     want = ops.prefix_attention(*dev)
-    a = mk.mk_prefix_attention_args()
     out = torch.zeros_like(dev[0])
-    for name, value in dict(device=0, batch=b, n_groups=1, max_pages=width, n_pages=b * width, n_q_heads=hq,
-                            n_kv_heads=hkv, head_dim=hd, type=mk.MK_BF16, scale=hd ** -0.5, q_token_stride=hq * hd,
-                            q=dev[0].data_ptr(), k_pool=dev[1].data_ptr(), v_pool=dev[2].data_ptr(),
-                            page_table=dev[3].data_ptr(), positions=dev[4].data_ptr(), group_start=dev[5].data_ptr(),
-                            prefix_lens=dev[6].data_ptr(), out=out.data_ptr()).items():
-        setattr(a, name, value)
+    a = c_arguments(dev, out)
     size, edge = mk.lib.mk_prefix_attention_workspace(ctypes.byref(a)), 1 << 20
     for fill in (0, 255):
         memory = torch.full((size + 2 * edge,), fill, dtype=torch.uint8, device=DEV)
@@ -269,3 +278,37 @@ def test_attention_stays_inside_its_workspace(lens, hq, hkv, prefix):
         assert (memory[:edge] == fill).all() and (memory[edge + size:] == fill).all()
         a.workspace_bytes = size - 1
         assert mk.lib.mk_prefix_attention(ctypes.byref(a), None) == mk.MK_ERR_CAPACITY
+
+
+# --------------------------------------------------- waits that run out --
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("hd,lens,hq,hkv,prefix", [
+    (64, (90, 200, 131), 4, 2, 64),                      # a block's share is a tile: it ends at once
+    (128, (900, 1000, 1100, 40), 4, 1, 830),             # more than one tile, two streams of one unit
+    (64, (1500,), 2, 1, 0),
+    (128, tuple(range(130, 130 + 40)), 16, 4, 128)])     # two tiles of rows, one warp a row in the join
+def test_attention_rows_of_a_wait_that_ran_out(hd, lens, hq, hkv, prefix, dtype):
+    """One block's tiles never come: its waits give up, the status says so, and the
+    rows that it held shares of are right all the same."""
+    args, want = attention_case(15, lens, hq, hkv, hd, dtype, prefix)
+    b = len(lens)
+    out, lse = torch.full_like(args[0], 9.0), torch.full((b, hq), 9.0, device=DEV)
+    status = ops.Status(DEV)
+    a = c_arguments(args, out, lse=lse.data_ptr(), status=status.word.data_ptr())
+    size = mk.lib.mk_prefix_attention_workspace(ctypes.byref(a))
+    work = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    a.workspace, a.workspace_bytes = work.data_ptr(), size
+    stream = torch.cuda.current_stream().cuda_stream
+    assert mk.lib.mk_prefix_attention_selftest(ctypes.byref(a), stream) == mk.MK_OK
+    rc, detail = status.check()
+    assert rc == mk.MK_ERR_TIMEOUT and detail[:2] == [mk.MK_OP_PREFIX_ATTENTION, 0]
+    check_attention(out, want, dtype)
+    # 32-bit scores and sums move the logarithm by 2e-5 (1 + the largest score)
+    assert ((lse.cpu().double() - want[1]).abs() <= 2e-5 * (1 + want[3])).all()
+    # the next call in the same workspace is as ever
+    out.fill_(9.0)
+    assert mk.lib.mk_prefix_attention(ctypes.byref(a), stream) == mk.MK_OK
+    status.check_ok()
+    assert torch.equal(out, ops.prefix_attention(*args))
+    check_attention(out, want, dtype)

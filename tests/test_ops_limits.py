@@ -33,3 +33,10 @@ def test_attention_workspace_goes_by_the_batch():
         now = size(batch=b, n_q_heads=16, n_kv_heads=4, head_dim=128)
         assert now > last, b
         last = now
+
+
+def test_attention_selftest_refusals():
+    call = mk.lib.mk_prefix_attention_selftest
+    assert call(None, None) == mk.MK_ERR_INVALID
+    assert call(byref(attention_args()), None) == mk.MK_ERR_INVALID                # no status word
+    assert call(byref(attention_args(status=4096, batch=-1)), None) == mk.MK_ERR_INVALID
