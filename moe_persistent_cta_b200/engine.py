@@ -67,6 +67,7 @@ class Decoder:
         self._ctx = ctx
         self.batch = 0
         self.max_pages = 0
+        self.planned = []       # cached tokens that the fused steps of the schedule reach, per entry
 
     # ------------------------------------------------------------------
     def build_schedule(self, seq_lens: Sequence[int], max_pages_per_seq: int,
@@ -78,6 +79,7 @@ class Decoder:
                         "mk_build_schedule")
         self.batch = B
         self.max_pages = int(max_pages_per_seq)
+        self.planned = [int(n) for n in plan_len] if plan_len is not None else [int(n) + 64 for n in seq_lens]
 
     def step(self, tokens: torch.Tensor, positions: torch.Tensor, page_table: torch.Tensor,
              seq_lens: torch.Tensor, logits: torch.Tensor, stream=None,

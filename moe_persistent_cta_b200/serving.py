@@ -175,13 +175,38 @@ def sampling_rules(sampling: Dict, rows: int, device) -> Dict[str, torch.Tensor]
             for name in sampling}
 
 
+# Bytes of keys and values a layer that steps with a shared prefix must save to
+# pay: their launches cost 25 to 33 us a layer.  30B-MoE shape, all 48 layers, us a
+# step fused / shared: 8 samples of 8192 tokens (117 MB saved) 8280 / 8800, of 16384
+# (235 MB) 9220 / 9030, of 32768 (470 MB) 10990 / 9700; 4 samples of 32768 (201 MB)
+# 7230 / 7550, of 65536 (403 MB) 9010 / 8550; 2 samples of 131072 (268 MB) 7400 / 8060.
+SHARED_SAVES = 300e6
+
+
+def takes_shared_steps(dec, prefix: int, last: int, shared: Optional[bool] = None) -> bool:
+    """Whether the samples of a prompt run as steps that read its first `prefix`
+    tokens once: where that saves more than the launches cost, and where the
+    schedule does not reach `last` cached tokens, which fused steps need."""
+    reached = all(n >= last for n in dec.planned)
+    if shared is False and not reached:
+        raise ValueError(f"the schedule is planned for {dec.planned} cached tokens, not {last}")
+    if shared is not None:
+        return shared
+    kv = 2 * dec.shape["n_kv_heads"] * dec.shape["head_dim"] * 2
+    return not reached or (dec.batch - 1) * prefix * kv > SHARED_SAVES
+
+
 def sample_prompt(dec, k_pool: torch.Tensor, v_pool: torch.Tensor, pool: PagePool,
                   prompt_pages: List[int], prompt_len: int, tokens: List[int], steps: int, *,
                   max_pages_per_seq: int, seed: int = 0, sampling: Optional[Dict] = None,
-                  stream=None) -> Dict:
+                  shared: Optional[bool] = None, stream=None) -> Dict:
     """Several samples of one cached prompt: sample i feeds tokens[i] and then
-    ``steps`` drawn tokens, reading the prompt's whole pages through one page
-    list, once per step for all samples (mk_decode_step_shared).
+    ``steps`` drawn tokens, its page list naming the prompt's whole pages.
+
+    shared: True: steps that read those pages once for all samples
+    (mk_decode_step_shared, whose queries are rounded to bf16); False: fused steps,
+    for which the schedule has to be planned for prompt_len + steps - 1 tokens;
+    None: whichever is faster (``takes_shared_steps``).
 
     The prompt's ``prompt_len`` tokens lie in ``prompt_pages`` of every layer's
     pools.  Where it ends inside a page, that page is copied for each sample;
@@ -200,6 +225,7 @@ def sample_prompt(dec, k_pool: torch.Tensor, v_pool: torch.Tensor, pool: PagePoo
     need = pages_for(prompt_len + steps)
     if need > max_pages_per_seq:
         raise ValueError("the samples outgrow the page table")
+    groups = takes_shared_steps(dec, whole * PAGE, prompt_len + max(steps, 1) - 1, shared)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     own: List[List[int]] = []
     try:
@@ -224,10 +250,11 @@ def sample_prompt(dec, k_pool: torch.Tensor, v_pool: torch.Tensor, pool: PagePoo
             logits = torch.empty((n, dec.shape["vocab"]), dtype=torch.float32, device=dev)
             u = torch.rand((steps, n), device=dev,
                            generator=torch.Generator(device=dev).manual_seed(seed))
-            dec.sample(steps, toks, lens, table_d, lens, logits, out, u, logprobs=logprobs,
-                       group_start=torch.tensor([0, n], **i32),
-                       prefix_lens=torch.tensor([whole * PAGE], **i32), stream=s,
-                       **sampling_rules(sampling or {}, n, dev))
+            rules = sampling_rules(sampling or {}, n, dev)
+            if groups:
+                rules.update(group_start=torch.tensor([0, n], **i32),
+                             prefix_lens=torch.tensor([whole * PAGE], **i32))
+            dec.sample(steps, toks, lens, table_d, lens, logits, out, u, logprobs=logprobs, stream=s, **rules)
         dec.check_ok()
     finally:
         s.synchronize()               # no step writes the pages any more, however far it came

@@ -5,8 +5,10 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from moe_persistent_cta_b200 import configs, engine, mk, ops, serving, synth
 from tests.gpu_common import MAX_ABS, REL_L2, TinyRig, compare_logits, to_dev
+from tests.oracle_io import array_kv, array_weights, oracle_shape
 from tests.test_gpu_shared import DEV, i32, shared_rig, shared_step
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +123,51 @@ def test_continuous_batching_on_another_stream_than_the_current_one():
         finally:
             dec.close()
     assert np.array_equal(runs[0], runs[1]) and np.array_equal(runs[0], runs[2])
+
+
+@pytest.mark.parametrize("prompt_len", [128, 150, 20])
+def test_samples_of_one_prompt_by_fused_and_by_shared_steps(prompt_len):
+    """Either kind of step draws from the oracle's logits; the kind is the one asked
+    for, or the faster one, or the one that the schedule's plan allows."""
+    shape = configs.TINY
+    n, max_pages, n_pages = 3, 6, 40
+    L, hkv, hd = shape["n_layers"], shape["n_kv_heads"], shape["head_dim"]
+    W = synth.make_weights(shape, 0, "cpu")
+    g = torch.Generator().manual_seed(4)
+    kc, vc = (torch.randn((L, n_pages, hkv, 64, hd), generator=g).to(torch.bfloat16) for _ in range(2))
+    k, v = kc.to(DEV), vc.to(DEV)
+    dec = engine.Decoder(shape, to_dev(W, DEV), k, v, max_batch=n)
+    first = [3, 700, 41]
+    took, sample = [], dec.sample
+    dec.sample = lambda *a, **kw: (took.append("group_start" in kw), sample(*a, **kw))
+    try:
+        pool = serving.PagePool(n_pages)
+        pages = pool.alloc(serving.pages_for(prompt_len))
+        rows = np.full((n, max_pages), -1, dtype=np.int32)
+        for i in range(n):                               # the oracle's own copies of the prompt
+            rows[i, :len(pages)] = pages
+        rows[:, len(pages)] = [30, 31, 32]
+        if prompt_len % 64:
+            for i in range(n):
+                rows[i, len(pages) - 1] = 33 + i
+                kc[:, 33 + i], vc[:, 33 + i] = kc[:, pages[-1]], vc[:, pages[-1]]
+        ref = oracle.decode_step(oracle_shape(shape), array_weights(W), array_kv(kc, vc), first, [prompt_len] * n, rows)
+        dec.build_schedule([prompt_len] * n, max_pages)
+        common = dict(max_pages_per_seq=max_pages, seed=2, sampling=dict(temperature=1.3))
+        for shared in (None, False, True):
+            r = serving.sample_prompt(dec, k, v, pool, pages, prompt_len, first, 1, shared=shared, **common)
+            err, rel = compare_logits(r["logits"].cpu().double().numpy(), ref)
+            assert err <= MAX_ABS and rel <= REL_L2, (shared, err, rel)
+        assert took == [False, False, True]
+        # steps past the plan: shared ones alone can
+        free, steps = pool.free_count(), 66
+        with pytest.raises(ValueError):
+            serving.sample_prompt(dec, k, v, pool, pages, prompt_len, first, steps, shared=False, **common)
+        r = serving.sample_prompt(dec, k, v, pool, pages, prompt_len, first, steps, **common)
+        assert took[-1] and ((r["tokens"] >= 0) & (r["tokens"] < shape["vocab"])).all()
+        assert pool.free_count() == free
+        dec.build_schedule([prompt_len] * n, max_pages, plan_len=[64 * max_pages - 1] * n)
+        r = serving.sample_prompt(dec, k, v, pool, pages, prompt_len, first, steps, **common)
+        assert not took[-1] and ((r["tokens"] >= 0) & (r["tokens"] < shape["vocab"])).all()
+    finally:
+        dec.close()

@@ -35,6 +35,7 @@ class Stream:
 def decoder():
     d = engine.Decoder.__new__(engine.Decoder)
     d.shape, d.batch, d.max_pages, d.device, d._ctx = dict(vocab=V), B, PAGES, 0, None
+    d.planned = [64 * PAGES] * B
     return d
 
 
@@ -112,3 +113,21 @@ def test_sample_prompt_refusals(kw):
     with pytest.raises(ValueError):
         serving.sample_prompt(decoder(), k, k, pool, pages, max_pages_per_seq=PAGES, **args)
     assert pool.free_count() == 18
+
+
+def test_shared_steps_where_they_save_more_than_they_cost():
+    d = decoder()
+    d.shape.update(n_kv_heads=4, head_dim=128)           # 2048 bytes a token and layer
+    takes = lambda n, prefix, last=100, **kw: (setattr(d, "batch", n), setattr(d, "planned", [10 ** 6] * n),  # noqa: E731
+                                               serving.takes_shared_steps(d, prefix, last, **kw))[2]
+    # as measured: 8 samples from 16384 .. 32768 on, 4 from 32768 .. 65536 on, 2 not at 131072, 1 never
+    assert [takes(8, p) for p in (0, 8192, 16384, 32768, 131072)] == [False, False, False, True, True]
+    assert [takes(4, p) for p in (16384, 32768, 65536)] == [False, False, True]
+    assert not takes(2, 131072) and not takes(1, 10 ** 7)
+    assert takes(2, 64, shared=True) and not takes(8, 131072, shared=False)
+    # fused steps cannot pass the schedule's plan
+    d.batch, d.planned = 2, [200, 190]
+    assert not serving.takes_shared_steps(d, 128, 190)
+    assert serving.takes_shared_steps(d, 128, 191) and serving.takes_shared_steps(d, 128, 191, True)
+    with pytest.raises(ValueError):
+        serving.takes_shared_steps(d, 128, 191, False)
