@@ -274,7 +274,8 @@ def prefix_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
     if q.dtype is not dtype:
         raise TypeError("q must have the pools' type")
     qs = q.stride()
-    if b and (qs[2] != 1 or qs[1] != hd or qs[0] % 8):
+    rows = qs[0] if b > 1 else hq * hd               # a stride that no element uses may be anything
+    if b and (qs[2] != 1 or (qs[1] != hd and hq > 1) or rows % 8):
         raise ValueError("q's heads must be adjacent and its token stride a multiple of 8")
     if hq < 1 or hq % hkv:
         raise ValueError("query heads must be a multiple of the kv heads")
@@ -297,7 +298,7 @@ def prefix_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
             work = q.new_empty(size, dtype=torch.uint8)
     a = _PACK_ATTENTION(
             dev, b, n, pages, n_pages, hq, hkv, hd, _TYPE[dtype],
-            1.0 / math.sqrt(hd) if scale is None else scale, q.data_ptr(), qs[0], k_pool.data_ptr(),
+            1.0 / math.sqrt(hd) if scale is None else scale, q.data_ptr(), rows, k_pool.data_ptr(),
             v_pool.data_ptr(), _array(page_table, _I32, "page_table", dev, (b, pages)),
             _array(positions, _I32, "positions", dev, (b,)),
             _array(group_start, _I32, "group_start", dev, (n + 1,)),

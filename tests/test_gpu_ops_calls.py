@@ -312,3 +312,22 @@ def test_attention_rows_of_a_wait_that_ran_out(hd, lens, hq, hkv, prefix, dtype)
     status.check_ok()
     assert torch.equal(out, ops.prefix_attention(*args))
     check_attention(out, want, dtype)
+
+
+# ---------------------------------------------------------------- strides --
+
+def test_attention_strides_of_single_entries_and_heads():
+    """Strides along a size of one say nothing: any value is accepted."""
+    args, want = attention_case(16, (90, 200), 1, 1, 64)
+    wide = torch.zeros((2, 3, 64), dtype=torch.bfloat16, device=DEV)
+    wide[:, 1:2] = args[0]
+    odd = torch.zeros(2 * 72 + 64, dtype=torch.bfloat16, device=DEV)
+    for q in (wide[:, 1:2], torch.as_strided(args[0], (2, 1, 64), (64, 5, 1))):
+        check_attention(ops.prefix_attention(q, *args[1:]), want)
+    one, want1 = attention_case(17, (150,), 4, 2, 64)
+    for q in (torch.as_strided(one[0], (1, 4, 64), (7, 64, 1)), torch.as_strided(one[0], (1, 4, 64), (0, 64, 1))):
+        check_attention(ops.prefix_attention(q, *one[1:]), want1)
+    for strides in ((72, 65, 1), (100, 64, 1), (8, 64, 1)):   # heads apart, rows that overlap or start off the boundary
+        with pytest.raises((ValueError, mk.MKError)):
+            ops.prefix_attention(torch.as_strided(odd, (2, 1 + (strides[1] == 65), 64), strides), args[1], args[2],
+                                 *args[3:])
