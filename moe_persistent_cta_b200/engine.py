@@ -57,7 +57,9 @@ class Decoder:
         t.w_down = arr(weights["w_down"])
         t.k_pool = arr([k_pool[l] for l in range(L)])
         t.v_pool = arr([v_pool[l] for l in range(L)])
-        self._inv_freq = None                       # of append_kv
+        # of append_kv, made here so that its first call may be captured
+        self._inv_freq, _ = ops.rope_frequencies(shape["head_dim"], shape.get("rope_theta", 1.0e4),
+                                                 device=k_pool.device)
         self._append_status = ops.Status(k_pool.device)
         self._appended = False                      # some call names that word
         self._tensors = (weights, k_pool, v_pool)   # keep caller tensors alive
@@ -209,9 +211,6 @@ class Decoder:
         ``ops.rope_append``'s.  Without a ``status`` of its own, a call's fault is
         the decoder's: the next ``check`` reports it."""
         _, k_pool, v_pool = self._tensors
-        if self._inv_freq is None:
-            self._inv_freq, _ = ops.rope_frequencies(
-                self.shape["head_dim"], self.shape.get("rope_theta", 1.0e4), device=k_pool.device)
         if status is None:
             status, self._appended = self._append_status, True
         ops.rope_append(None, k, v, positions, page_table, k_pool[layer], v_pool[layer],

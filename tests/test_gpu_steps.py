@@ -171,3 +171,28 @@ def test_samples_of_one_prompt_by_fused_and_by_shared_steps(prompt_len):
         assert not took[-1] and ((r["tokens"] >= 0) & (r["tokens"] < shape["vocab"])).all()
     finally:
         dec.close()
+
+
+def test_append_kv_first_called_in_a_capture():
+    shape = configs.TINY
+    hkv, hd = shape["n_kv_heads"], shape["head_dim"]
+    r = TinyRig(shape, [100], seed=6)
+    try:
+        k = torch.randn((3, hkv, hd), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+        table, seq, pos = r.table.to(DEV), i32([0, 0, 0]), i32([100, 101, 102])
+        ops.rope_append(None, k, k, pos, table, r.kd[0].clone(), r.vd[0].clone(), ops.rope_frequencies(hd)[0], seq=seq)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            r.dec.append_kv(1, k, k, pos, table, seq=seq)
+        want_k, want_v = r.kd[1].clone(), r.vd[1].clone()
+        graph.replay()
+        r.dec.check_ok()
+        ops.rope_append(None, k, k, pos, table, want_k, want_v, ops.rope_frequencies(hd)[0], seq=seq)
+        assert torch.equal(r.kd[1], want_k) and torch.equal(r.vd[1], want_v)
+        pos.copy_(i32([100, -5, 102]))                   # a replayed call's fault reaches the decoder too
+        graph.replay()
+        rc, d = r.dec.check()
+        assert rc == mk.MK_ERR_DEVICE and d[1:4] == [mk.MK_OP_ROPE_APPEND, 1, -5]
+        r.dec.check_ok()
+    finally:
+        r.close()
