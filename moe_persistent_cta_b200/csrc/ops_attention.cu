@@ -1206,7 +1206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Row (b, hq) from its own tokens alone, one warp, HD / 32 columns per lane:
 // what the tiles gave is not finite.  Slow, and right whatever the memory of
-// other entries holds.
+// other entries holds.  `acc` is kept as the weighted mean of the values so far,
+// which stays in range where their sum would not (bf16 values near 3e38).
 template <typename T, int HD>
 __device__ __noinline__ void row_alone(const AttnParams& p, int b, int hq, int group, float* acc, float* m_out,
                                        float* l_out) {
@@ -1239,9 +1240,13 @@ __device__ __noinline__ void row_alone(const AttnParams& p, int b, int hq, int g
     const float mn = fmaxf(m, s);
     const float f = m == mn ? 1.0f : ex2(m - mn), w = s == -INFINITY ? 0.0f : ex2(s - mn);
     m = mn;
-    l = fmaf(l, f, w);
+    const float before = l * f;
+    l = before + w;                      // 1 or more behind the first score
+    if (l != 0.0f) {
+      const float fo = before / l, fw = w / l;
 #pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] = fmaf(w, there ? to_float(v[i]) : 0.0f, acc[i] * f);
+      for (int i = 0; i < C; ++i) acc[i] = fmaf(fw, there ? to_float(v[i]) : 0.0f, acc[i] * fo);
+    }
   }
   *m_out = m;
   *l_out = l;
@@ -1388,8 +1393,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps<W>, W > 1 ? 1 : 8) join_kernel
   float size = 0.0f;
 #pragma unroll
   for (int i = 0; i < C; ++i) size += fabsf(acc[i]);
-  if (__any_sync(kFull, !(size < INFINITY) || !(l < INFINITY))) row_alone<T, HD>(p, b, hq, e.group, acc, &m, &l);
-  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays
+  const bool alone = __any_sync(kFull, !(size < INFINITY) || !(l < INFINITY));
+  if (alone) row_alone<T, HD>(p, b, hq, e.group, acc, &m, &l);
+  const float inv = alone ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
   for (int i = 0; i < C; ++i) acc[i] *= inv;
   if (p.sink.out) {

@@ -331,3 +331,25 @@ def test_attention_strides_of_single_entries_and_heads():
         with pytest.raises((ValueError, mk.MKError)):
             ops.prefix_attention(torch.as_strided(odd, (2, 1 + (strides[1] == 65), 64), strides), args[1], args[2],
                                  *args[3:])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_values_near_the_largest(hd):
+    """Finite values whose weighted sum leaves the 32-bit range: their mean does not."""
+    g = gen(18)
+    lens, width = (300, 500), 8
+    kp, vp = (torch.randn((2 * width, 2, 64, hd), generator=g) for _ in range(2))
+    vp = (vp.sign() * (2.0 + vp.abs().clamp(max=1.3)) * 1e38).to(torch.bfloat16)
+    vp[:, :, :, 0] = torch.finfo(torch.bfloat16).min     # a column of the type's lowest value
+    kp, q = kp.to(torch.bfloat16), torch.randn((2, 4, hd), generator=g).to(torch.bfloat16)
+    assert torch.isfinite(vp).all()
+    table = torch.randperm(2 * width, generator=g).view(2, width).to(torch.int32)
+    pos = [n - 1 for n in lens]
+    out, lse, mass, high = ops_oracle.attention(q, kp, vp, table, pos, [0, 2], [128], hd ** -0.5)
+    assert torch.isfinite(out).all()
+    got_lse = torch.zeros((2, 4), device=DEV)
+    got = ops.prefix_attention(q.to(DEV), kp.to(DEV), vp.to(DEV), table.to(DEV), i32(pos), i32([0, 2]), i32([128]),
+                               lse=got_lse)
+    assert torch.isfinite(got).all()
+    check_attention(got, (out, lse, mass, high))
+    assert ((got_lse.cpu().double() - lse).abs() <= 2e-5 * (1 + high)).all()
