@@ -784,6 +784,11 @@ mk_status mk_decode_sample(mk_ctx* c, int32_t n_steps, int32_t* tokens, int32_t*
   if (n_steps > 0) {
     MK_CUDA(cudaSetDevice(c->device));
     MK_TRY(refuse_capture(static_cast<cudaStream_t>(stream)));
+    if (c->cut_short) return MK_ERR_STATE;
+    if (!tokens || !positions || !page_table || !seq_lens || !logits) return MK_ERR_INVALID;
+    // once is enough: every step adds one to both
+    if (positions != seq_lens)
+      MK_CUDA(mk::ops::check_equal(positions, seq_lens, c->B, c->d_status, static_cast<cudaStream_t>(stream)));
   }
   for (int32_t i = 0; i < n_steps; ++i) {
     const size_t at = (size_t)i * c->B;

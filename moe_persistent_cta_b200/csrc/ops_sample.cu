@@ -874,11 +874,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (p.logprobs) p.logprobs[b] = logprob;
     if (p.next_token) {
       p.next_token[b] = token < 0 ? 0 : token;   // the step's embedding needs a token id
-      const int pos = p.position[b], len = p.seq_len[b];
-      // the entries advance alone, so there are no prefill groups
-      if (pos != len) report(p.status, MK_ERR_DEVICE, MK_OP_SAMPLE, b, pos, len);
+      const int pos = p.position[b];
       p.position[b] = pos + 1;
-      if (p.seq_len != p.position) p.seq_len[b] = len + 1;
+      if (p.seq_len != p.position) p.seq_len[b] += 1;
     }
   }
   // No barrier: behind the last one no block touches another's memory.

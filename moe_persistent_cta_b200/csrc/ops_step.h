@@ -25,6 +25,12 @@ mk_status prefix_attention(const mk_prefix_attention_args* args, const StepSink&
 mk_status sample(const mk_sample_args* args, int32_t* next_token, int32_t* position, int32_t* seq_len,
                  cudaStream_t stream);
 
+// Reports (MK_ERR_DEVICE, MK_OP_SAMPLE) an entry whose position is not its
+// sequence's length: sampled steps advance every entry alone.  Ahead of them, since
+// the same test in the sampling kernel cost every call of it 1 %.
+cudaError_t check_equal(const int32_t* position, const int32_t* seq_len, int n, int32_t* status,
+                        cudaStream_t stream);
+
 // counters[pairs[2 i]] += pairs[2 i + 1] for i < n.
 cudaError_t add_to_counters(uint32_t* counters, const int32_t* pairs, int n, cudaStream_t stream);
 

@@ -58,7 +58,7 @@ cudaError_t cudaGetDriverEntryPoint(const char*, void** f, unsigned long long, c
 }
 
 // ---- the kernels: counted, failing when told to ----
-static int g_interp = 0, g_append = 0, g_attend = 0, g_sample = 0, g_added = 0;
+static int g_interp = 0, g_append = 0, g_attend = 0, g_sample = 0, g_added = 0, g_checked = 0;
 static int g_fail_interp = -1, g_fail_append = -1, g_fail_attend = -1, g_fail_sample = -1;
 static uint32_t g_epoch = 0;
 static uint32_t* g_counters = nullptr;
@@ -77,6 +77,10 @@ mk_status prefix_attention(const mk_prefix_attention_args*, const StepSink&, cud
 }
 mk_status sample(const mk_sample_args*, int32_t*, int32_t*, int32_t*, cudaStream_t) {
   return g_sample++ == g_fail_sample ? MK_ERR_CUDA : MK_OK;
+}
+cudaError_t check_equal(const int32_t*, const int32_t*, int, int32_t*, cudaStream_t) {
+  ++g_checked;
+  return cudaSuccess;
 }
 cudaError_t add_to_counters(uint32_t* c, const int32_t* pairs, int n, cudaStream_t) {
   ++g_added;
@@ -134,7 +138,7 @@ CASES = {
   CHECK(shared(c) == MK_OK && g_interp == L + 1 && g_append == L && g_attend == L && g_added == 1 && g_epoch == 1);
   CHECK(step(c) == MK_OK && g_epoch == 2 && mk_check(c, nullptr, nullptr) == MK_OK);
   clear_tally();
-  CHECK(sampled(c, 1) == MK_OK && g_sample == STEPS && g_attend == STEPS * L && g_epoch == 2 + STEPS);
+  CHECK(sampled(c, 1) == MK_OK && g_checked == 1 && g_sample == STEPS && g_attend == STEPS * L && g_epoch == 2 + STEPS);
   CHECK(sampled(c, 0) == MK_OK && g_sample == 2 * STEPS && g_epoch == 2 + 2 * STEPS);
 """,
     "captured": r"""
@@ -145,7 +149,7 @@ CASES = {
   const int allocs = g_allocs;
   CHECK(shared(c) == MK_ERR_STATE && sampled(c, 1) == MK_ERR_STATE && sampled(c, 0) == MK_ERR_STATE);
   CHECK(sampled(c, 1, 0) == MK_OK);       // no step: nothing to launch
-  CHECK(g_interp == 0 && g_added == 0 && g_sample == 0 && g_allocs == allocs);
+  CHECK(g_interp == 0 && g_added == 0 && g_sample == 0 && g_checked == 0 && g_allocs == allocs);
   g_capture = cudaStreamCaptureStatusNone;
   CHECK(shared(c) == MK_OK && g_epoch == 2);
 """,
