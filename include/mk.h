@@ -375,7 +375,10 @@ mk_status mk_rope_append(const mk_rope_append_args* args, void* stream);
 
 /* Attention of one query token per batch entry over the paged cache, for
  * batches whose entries share prefixes: the shared tokens are read once for
- * all of a group's entries.
+ * every 2 x floor(128 x n_kv_heads / n_q_heads) consecutive entries of a group
+ * (64 entries with 4 query heads to a KV head), not once for each.
+ * Scores, sums and the running result are 32-bit; the weights are rounded to `type`
+ * before they meet the values.
  *   q           [batch] rows of n_q_heads heads of head_dim (64 or 128)
  *               elements of `type` (bf16 or fp16); token stride in elements (a
  *               multiple of 8), heads adjacent; 16-byte aligned

@@ -9,15 +9,17 @@
 // into [-pi, pi] in 64 bits, since at position 2^18 one 32-bit rounding step
 // of the angle is already 2^-6; the sine and cosine are then 32-bit.
 //
-// Bound: memory (each row is read and written once, no reuse), and next to it
-// the instructions that turn the pairs.  A warp takes a token, or some heads of
+// Bound: each row is read and written once, without reuse, so memory is the floor.
+// What it is bound by now is the chain of a warp: its loads, its look-ups, its
+// stores, with 24 warps on a multiprocessor (80 registers a thread).  A warp takes a token, or some heads of
 // one: it asks for all its rows first (16 columns a lane and head, two 16-byte
 // loads of 16-bit rows); while they are on their way it looks up the token's
 // place and forms its sines and cosines, two a lane, which a lane then holds in
 // registers for all its heads.  No warp waits for another.  8192 tokens of 24
-// heads of 128 in bf16 take 21.3 us (4.7 TB/s), 16381 in fp16 with half of each
-// head rotated 37.6 us (5.4 TB/s, 83 % of a plain copy); single tokens are bound
-// by the launch.
+// heads of 128 in bf16 take 21.3 us (4.7 TB/s; memory is 31 % busy, as most of what
+// is written stays in the L2 cache, and the multiprocessors 44 %), 16381 in fp16 with
+// half of each head rotated 37.1 us (5.4 TB/s, 84 % of a plain copy); single tokens
+// are bound by the launch.
 #include "ops_common.cuh"
 
 namespace mk {

@@ -1,6 +1,6 @@
 // ops_attention.cu -- attention of one query token per batch entry over the
 // paged cache, with the pages of a prefix that a group of entries shares read
-// once for the whole group.
+// once for as many of them as two tiles of rows hold.
 //
 // For entry b and query head h, with seen = positions[b] + 1:
 //   o = sum_t exp(s_t - lse) v_t,  s_t = scale q . k_t,  t < seen,
@@ -21,7 +21,8 @@
 // 5300 cycles with two tiles of rows and 5000 with one entry's.)  Each block finds
 // its stretch from the device arrays: the host needs no lengths, and a captured
 // graph replays with new ones.  A block's share of a unit leaves partial results
-// (O, m, l); a second launch adds them up.
+// (O, m, l); a second launch adds them up.  A group of more than 2 x MB entries is
+// several units, and its prefix is read as often.
 //
 // One block: a TMA warp streams K and V tiles, two warps issue tcgen05 MMAs,
 // and two groups of four warps hold a softmax row per thread.  S = Q K^T and O
@@ -33,14 +34,21 @@
 // with fewer they are alternate tiles of tokens of the same rows, two partial
 // results.
 //
+// Sums, maxima and O are 32-bit.  P alone is rounded to the cache's type, since
+// both operands of an MMA are of one 16-bit type and V is the cache's: each weight
+// is off by at most half a step, a row by at most half a step of its weighted |v|
+// (against 64 bits, bf16: 0.0023 of the result's norm, with P in 32 bits 0.0017, of
+// which the output's own rounding is 0.0017).  P in two parts would double P V.
+//
 // What bounds it: 256 entries on 32768 shared and up to 300 own tokens each (16
-// query heads of 128, 4 KV heads, bf16) take 132 us, 0.52 PFLOP/s, the tensor pipe
-// a third busy.  The MMAs alone, without the softmax, take 119 of them: with 64
-// columns of S each Q K^T reads three times its share from shared memory (Q has no
-// room in tensor memory beside S and O), and with 128 S cannot be replaced by
-// halves (135).  One MMA warp that also passed over the other stream's tiles: 138.
-// Few rows: 8 entries on 8192 tokens 17.7 us, of which 5 find the block's share of
-// the work and 5 add up the partial results.
+// query heads of 128, 4 KV heads, bf16) take 128 us (124 to 132, by the clocks), 0.54
+// PFLOP/s, the tensor pipe a third busy.  The MMAs alone, without the softmax, take
+// about nine tenths of that (119 of 132): with 64 columns of S each Q K^T reads
+// three times its share from shared memory (Q has no room in tensor memory beside S
+// and O), and with 128 S cannot be replaced by halves (135).  One MMA warp that also
+// passed over the other stream's tiles: 138.  Few rows: 8 entries on 8192 tokens
+// 17.7 us, of which 5 find the block's share of the work and 5 add up the partial
+// results.
 //
 // Values that are no numbers.  A masked weight is 0, and 0 x infinity is NaN:
 // V's rows outside a unit's tokens are cleared in shared memory, but a row can
@@ -1447,9 +1455,14 @@ int sm_count(int device) {
   return count[device];
 }
 
-// Rows up to which eight warps join one: few rows have many shares each, and as
-// many blocks run at once (128 rows: 17.4 us in all; 976 rows: 41 us, with one
-// warp a row 31).
+// Rows up to which eight warps join one.  Two such blocks run on a multiprocessor,
+// 296 in all.  Up to there eight warps were faster in every case measured (heads of
+// 64 and 128; 128 rows on 8192 tokens 17.8 us, with one warp 27.7; 288 rows on 1000
+// tokens 16.7 and 17.2), from 640 rows on slower in every one (8192: 35.7 and 30.6;
+// 1000: 28.4 and 20.9).  Between, rows of many shares gain (448 rows on 8192: 30.0
+// and 34.2, on 32768: 35.3 and 40.8) and rows of few lose (on 1000: 23.8 and 20.2, in
+// 4 groups on 4999: 30.8 and 28.5).  The host does not know the lengths: this is
+// where the two even out.
 constexpr unsigned kWideJoin = 448;
 
 constexpr int kMaxBlocks = 160;      // at least the device's multiprocessors

@@ -148,7 +148,8 @@ def rope_frequencies(rotary_dim: int, theta: float = 1.0e4, *, scaling: Optional
     "parts": pairs that turn at least ``fast_turns`` times over trained_len
     are kept, those that turn at most ``slow_turns`` times divided by factor,
     those between blended linearly in their number of turns, with magnitude
-    0.1 ln(factor) + 1."""
+    0.1 ln(factor) + 1.  (A model trained with a blend that is linear in the pair's
+    index, as some are, needs its own table: any float64 tensor will do.)"""
     if rotary_dim < 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even")
     if not (theta > 0 and factor >= 1.0):
@@ -251,8 +252,8 @@ def prefix_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor
                      scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                      lse: Optional[torch.Tensor] = None, status: Optional[Status] = None,
                      stream=None) -> torch.Tensor:
-    """Attention of one query token per batch entry over the paged cache,
-    shared prefixes read once per group (mk_prefix_attention).
+    """Attention of one query token per batch entry over the paged cache, shared
+    prefixes read once for many entries of a group (mk_prefix_attention).
 
     q [batch][query heads][hd] of the pools' type; positions int32[batch]: entry
     b attends to tokens 0 .. positions[b] of its sequence (-1: to none, output
