@@ -256,11 +256,14 @@ def sample_prompt(dec, k_pool: torch.Tensor, v_pool: torch.Tensor, pool: PagePoo
                              prefix_lens=torch.tensor([whole * PAGE], **i32))
             dec.sample(steps, toks, lens, table_d, lens, logits, out, u, logprobs=logprobs, stream=s, **rules)
         dec.check_ok()
+        with torch.cuda.stream(s):
+            result = {"tokens": out.cpu().numpy(), "logprobs": logprobs.cpu().numpy(), "logits": logits}
+        logits.record_stream(torch.cuda.current_stream(dev))   # whose memory is s's
     finally:
         s.synchronize()               # no step writes the pages any more, however far it came
         for pages in own:
             pool.release(pages)
-    return {"tokens": out.cpu().numpy(), "logprobs": logprobs.cpu().numpy(), "logits": logits}
+    return result
 
 
 def run_continuous(dec, shape: Dict, k_pool: torch.Tensor, v_pool: torch.Tensor, slots: int,

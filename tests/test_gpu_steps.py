@@ -196,3 +196,36 @@ def test_append_kv_first_called_in_a_capture():
         r.dec.check_ok()
     finally:
         r.close()
+
+
+def test_logits_of_sample_prompt_outlive_their_release():
+    """Logits that the current stream still reads are not written by the next call
+    on the samples' stream."""
+    shape = configs.TINY
+    n, max_pages, n_pages = 3, 6, 40
+    kshape = (shape["n_layers"], n_pages, shape["n_kv_heads"], 64, shape["head_dim"])
+    g = torch.Generator().manual_seed(9)
+    k, v = (torch.randn(kshape, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    dec = engine.Decoder(shape, to_dev(synth.make_weights(shape, 0, "cpu"), DEV), k, v, max_batch=n)
+    try:
+        dec.build_schedule([100] * n, max_pages)
+        pool, side = serving.PagePool(n_pages), torch.cuda.Stream()
+        pages = pool.alloc(2)
+        run = lambda first: serving.sample_prompt(dec, k, v, pool, pages, 100, first, 1, max_pages_per_seq=max_pages,  # noqa: E731
+                                                  stream=side)
+        torch.cuda.synchronize()
+        want, other = run([3, 700, 41])["logits"].clone(), run([5, 6, 7])["logits"].clone()
+        kept = torch.empty_like(want)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.Stream()):     # the library's status copy waits for the default one
+            logits = run([3, 700, 41])["logits"]
+            at = logits.data_ptr()
+            torch.cuda._sleep(400_000_000)
+            kept.copy_(logits)
+            del logits
+            again = run([5, 6, 7])["logits"]
+            assert again.data_ptr() != at
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want) and torch.equal(again, other) and not torch.equal(want, other)
+    finally:
+        dec.close()
